@@ -401,6 +401,94 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
                                     dq_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (OCP Microscaling Formats v1.0, MXFP4, and
+ * the two-level block-16 form with e4m3 scales), quantization and the layer
+ *     out = bf16( acc * s_row * s_col + bias )
+ * with both operands in 4 bits, as dq_quantize_rows / dq_int8_linear are for 8.
+ *
+ * Codes: e2m1 (sign, two exponent bits with bias 1, one mantissa bit: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6), two per byte along the features: byte j of a row holds
+ * feature 2j in its low nibble and 2j + 1 in its high nibble.
+ *   fmt DQ_FP4_MX: blocks of 32 features; scale byte E (ue8m0, 2^(E - 127)),
+ *     E = floor(log2 a) - 2 + 127 clamped to 0..254, a the block's largest
+ *     magnitude; code = e2m1(x / 2^(E - 127)), round to nearest, ties to even,
+ *     saturating at 6.  No row scale.
+ *   fmt DQ_FP4_NV: row scale s = the least power of two with max|row| <=
+ *     2688 s (2688 = 6 * 448), at least 2^-110 (fp32); blocks of 16 features
+ *     with an e4m3 scale d = e4m3(fp32((a / s) / 6)); code = e2m1(x / (d s))
+ *     decided on the exact quotient, 0 where d = 0; the value is e2m1 * d * s.
+ * Codes, block scales and row scales are bit-equal to a scalar evaluation of
+ * these definitions.  A block (MX) or row (NV) with a NaN or an infinity gets
+ * a NaN scale (E = 255; s = NaN, its block scales and codes 0), so every
+ * product computed from it is NaN.
+ *
+ * Block scales are stored in tiles of 128 rows x 4 blocks, 512 bytes each,
+ * tile (row block, block group) row-major: byte 16 (r % 32) + 4 ((r % 128) /
+ * 32) + b % 4 of tile (r / 128, b / 4).  dq_fp4_scales_size() is the buffer's
+ * size; dq_fp4_tile_scales converts the plain [rows, K / block] form.  Bytes
+ * past the last row or block of a tile are written as 0; bytes past the last
+ * BLOCK must be finite scales when a caller fills the buffer itself.
+ *
+ * dq_quantize_rows_fp4: x bf16 [M, K] (row stride ldx) -> q [M, K/2] (row
+ *   stride ldq bytes), sf, s_row fp32 [M] (NV; ignored for MX, may be NULL).
+ *   Rows with ldx % 8 == 0, a 16-byte aligned x, 4-byte aligned q and ldq and
+ *   K <= 16384 take the single-pass kernel, others a slower one.
+ * dq_quantize_weight_fp4: the same for fp32 rows (output channels).
+ * dq_fp4_dequantize: out bf16 [M, K] = bf16(fp32(e2m1 * d) * s); s may be
+ *   NULL (1).  Exact for what the quantizers write.
+ * dq_fp4_linear: acc[m, n] = sum over blocks of sfa sfw sum a w on the tensor
+ *   cores (tcgen05.mma kind::mxf4nvf4.block_scale, fp32 accumulators);
+ *   DQ_OUT_BF16: out = bf16(((acc * s_row[m]) * s_col[n]) + bias[n]), each op
+ *   rounded on its own (s_row, s_col may be NULL: 1; bias NULL: no addition);
+ *   DQ_OUT_F32: out = acc.  A, W contiguous.  The order of the fp32 sum is the
+ *   hardware's and the schedule's; it does not change from call to call.
+ * Requirements: K % 32 == 0, N % 8 == 0, M >= 0, M, N, K <= 2^30; A, W, sf,
+ * out, s_col and bias 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+enum { DQ_FP4_MX = 0, DQ_FP4_NV = 1 };
+
+DQ_API size_t dq_fp4_scales_size(int64_t rows, int64_t K, int fmt);
+DQ_API dq_status dq_quantize_rows_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, int fmt, uint8_t* q,
+                                      int64_t ldq, uint8_t* sf, float* s_row, dq_stream_t stream);
+DQ_API dq_status dq_quantize_weight_fp4(const float* w, int64_t N, int64_t K, int64_t ldw, int fmt, uint8_t* wq,
+                                        int64_t ldwq, uint8_t* sf, float* s_col, dq_stream_t stream);
+DQ_API dq_status dq_fp4_dequantize(const uint8_t* q, const uint8_t* sf, const float* s, int64_t M, int64_t K, int fmt,
+                                   void* out_bf16, dq_stream_t stream);
+DQ_API dq_status dq_fp4_tile_scales(const uint8_t* scales, int64_t rows, int64_t K, int fmt, uint8_t* sf,
+                                    dq_stream_t stream);
+DQ_API dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float* s_row, int64_t M, int64_t K,
+                               const uint8_t* W, const uint8_t* sfw, const float* s_col, int64_t N, int fmt,
+                               const void* bias_bf16, void* out, dq_out_dtype out_dtype, dq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit activation checkpoints: a layer's bf16 input kept for the backward
+ * pass in half the bytes.
+ *
+ * Blocks of 32 consecutive tokens of one feature share a ue8m0 scale byte E =
+ * floor(log2 a) + 127 clamped to 0..254 (a the block's largest magnitude);
+ * code q = rint(64 x / 2^(E - 127)), ties to even, clamped to +-127; the value
+ * is q 2^(E - 133), exact in bf16 (the MXINT8 element and scale of OCP
+ * Microscaling Formats v1.0).  A block with a NaN or an infinity has E = 255
+ * and codes 0 and reads back as NaN.
+ * Layout: codes int8 [2 ceil(M / 32)][K][16] (16 tokens of a feature are 16
+ * contiguous bytes), scales uint8 [ceil(M / 32)][K]; dq_act8_codes_size() and
+ * dq_act8_scales_size() are the bytes.  Tokens past M in the last block have
+ * code 0.
+ *
+ * dq_act8_pack: x bf16 [M, K] (row stride ldx, any 2-byte aligned address;
+ *   8-byte aligned rows take wide loads) -> codes, scales.
+ * dq_act8_unpack: codes, scales -> out bf16 [M, K] contiguous.
+ * Requirements: K % 16 == 0, M >= 0, M, K <= 2^30; codes, scales and out
+ * 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+DQ_API size_t dq_act8_codes_size(int64_t M, int64_t K);
+DQ_API size_t dq_act8_scales_size(int64_t M, int64_t K);
+DQ_API dq_status dq_act8_pack(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, int8_t* codes, uint8_t* scales,
+                              dq_stream_t stream);
+DQ_API dq_status dq_act8_unpack(const int8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out_bf16,
+                                dq_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Measurement knobs.  Process-wide settings read by every later launch from
  * any host thread (relaxed atomics); they change which schedule or kernel a
  * call uses, never its result.  For benchmarks and tests of the alternative

@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(_HERE, "libdq.so")
 DQ_OK, DQ_ERR_INVALID_ARG, DQ_ERR_UNSUPPORTED, DQ_ERR_CUDA, DQ_ERR_TIMEOUT = range(5)
 DQ_OUT_BF16, DQ_OUT_S32, DQ_OUT_F32 = 0, 1, 2
 DQ_HQQ_S4 = 1
+DQ_FP4_MX, DQ_FP4_NV = 0, 1
 
 # C prototypes: (name, restype, argtypes)
 _P, _I64, _I32, _SZ, _U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
@@ -62,6 +63,16 @@ _PROTOS = {
     "dq_s24_int8_linear": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _I64, _P, _P, _I32, _P, _SZ, _P]),
     "dq_hqq_linear": (_I32, [_P, _I64, _P, _P, _P, _I64, _I64, _I32, _I32, _P, _P, _SZ, _P]),
     "dq_hqq_linear_t": (_I32, [_P, _I64, _P, _P, _P, _I64, _I64, _I32, _I32, _P, _P, _SZ, _P]),
+    "dq_fp4_scales_size": (_SZ, [_I64, _I64, _I32]),
+    "dq_quantize_rows_fp4": (_I32, [_P, _I64, _I64, _I64, _I32, _P, _I64, _P, _P, _P]),
+    "dq_quantize_weight_fp4": (_I32, [_P, _I64, _I64, _I64, _I32, _P, _I64, _P, _P, _P]),
+    "dq_fp4_dequantize": (_I32, [_P, _P, _P, _I64, _I64, _I32, _P, _P]),
+    "dq_fp4_tile_scales": (_I32, [_P, _I64, _I64, _I32, _P, _P]),
+    "dq_fp4_linear": (_I32, [_P, _P, _P, _I64, _I64, _P, _P, _P, _I64, _I32, _P, _P, _I32, _P]),
+    "dq_act8_codes_size": (_SZ, [_I64, _I64]),
+    "dq_act8_scales_size": (_SZ, [_I64, _I64]),
+    "dq_act8_pack": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "dq_act8_unpack": (_I32, [_P, _P, _I64, _I64, _P, _P]),
 }
 
 
@@ -642,6 +653,232 @@ def dq_s24_int8_linear(A, s_row, values, meta, s_col, bias=None, out=None, out_d
         ws_ptr, ws_bytes = _ptr(workspace), workspace.numel()
     _check(lib.dq_s24_int8_linear(_ptr(A), _ptr(s_row), M, K, _ptr(values), _ptr(meta), _ptr(s_col), N, _ptr(bias),
                                   _ptr(out), code, ws_ptr, ws_bytes, _stream(stream)), "dq_s24_int8_linear")
+    return out
+
+
+# ---------------------------------------------------------------- 4-bit microscaled
+
+def _fp4_fmt(fmt) -> int:
+    if fmt in ("mx", "mxfp4"):
+        return DQ_FP4_MX
+    if fmt in ("nv", "nvfp4"):
+        return DQ_FP4_NV
+    raise ValueError(f"fmt {fmt!r}: expected 'mx' or 'nv'")
+
+
+def _fp4_scale_shape(rows: int, K: int, code: int):
+    g = 64 if code == DQ_FP4_NV else 128
+    return ((rows + 127) // 128, (K + g - 1) // g, 512)
+
+
+def _same_device(first: torch.Tensor, **others):
+    """Every tensor of a call on one device, and that device the current one
+    (a kernel is launched on the current device)."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name}: on {t.device}, expected {first.device}")
+
+
+def _rows(x: torch.Tensor, name: str) -> int:
+    """Row stride of a [rows, width] tensor with contiguous rows."""
+    if x.shape[1] != 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+
+
+def dq_fp4_scales_size(rows: int, K: int, fmt="nv") -> int:
+    """Bytes of the tiled block scales of a [rows, K] matrix (0: unsupported)."""
+    return int(lib.dq_fp4_scales_size(rows, K, _fp4_fmt(fmt)))
+
+
+def _quantize_fp4(fn, name, x, dtype, fmt, q, sf, s, stream):
+    code = _fp4_fmt(fmt)
+    _need(x, dtype, "x", 2)
+    ld = _rows(x, "x")
+    M, K = x.shape
+    if K < 1 or K % 32 != 0:
+        raise ValueError(f"x: the row length must be a positive multiple of 32, got {K}")
+    shape = _fp4_scale_shape(M, K, code)
+    if q is None:
+        q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    if sf is None:
+        sf = torch.empty(shape, dtype=torch.uint8, device=x.device)
+    if s is None and code == DQ_FP4_NV:
+        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _need(q, torch.uint8, "q", 2)
+    _need(sf, torch.uint8, "sf", 3)
+    _contig(sf, "sf")
+    if tuple(q.shape) != (M, K // 2) or tuple(sf.shape) != shape:
+        raise ValueError(f"q must be {(M, K // 2)} and sf {shape}")
+    if code == DQ_FP4_NV:
+        _need(s, torch.float32, "row scales", 1)
+        _contig(s, "row scales")
+        if s.numel() != M:
+            raise ValueError("row scales: one per row")
+    elif s is not None:
+        raise ValueError("the mx format has no row scales")
+    _same_device(x, q=q, sf=sf, s=s)
+    _check(fn(_ptr(x), M, K, ld, code, _ptr(q), _rows(q, "q"), _ptr(sf), _ptr(s), _stream(stream)), name)
+    return q, sf, s
+
+
+def dq_quantize_rows_fp4(x: torch.Tensor, fmt="nv", q: torch.Tensor = None, sf: torch.Tensor = None,
+                         s_row: torch.Tensor = None, stream=None):
+    """Dynamic 4-bit quantization of activations: x bf16 [M, K] (row stride
+    x.stride(0), K % 32 == 0) -> (q uint8 [M, K/2], two e2m1 codes per byte; sf
+    uint8 [ceil(M/128), blocks/4, 512], the block scales in tiles; s_row fp32
+    [M] for "nv", None for "mx")."""
+    return _quantize_fp4(lib.dq_quantize_rows_fp4, "dq_quantize_rows_fp4", x, torch.bfloat16, fmt, q, sf, s_row, stream)
+
+
+def dq_quantize_weight_fp4(w: torch.Tensor, fmt="nv", wq: torch.Tensor = None, sf: torch.Tensor = None,
+                           s_col: torch.Tensor = None, stream=None):
+    """4-bit weight: w fp32 [N, K] -> (wq uint8 [N, K/2], sf, s_col fp32 [N] or None)."""
+    return _quantize_fp4(lib.dq_quantize_weight_fp4, "dq_quantize_weight_fp4", w, torch.float32, fmt, wq, sf, s_col,
+                         stream)
+
+
+def dq_fp4_tile_scales(scales: torch.Tensor, fmt="nv", sf: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Block scale bytes uint8 [rows, K/block] (ue8m0 for "mx", e4m3 for "nv")
+    -> the tiled layout the kernels read."""
+    code = _fp4_fmt(fmt)
+    _need(scales, torch.uint8, "scales", 2)
+    _contig(scales, "scales")
+    R, G = scales.shape
+    K = G * (16 if code == DQ_FP4_NV else 32)
+    shape = _fp4_scale_shape(R, K, code)
+    if sf is None:
+        sf = torch.empty(shape, dtype=torch.uint8, device=scales.device)
+    _need(sf, torch.uint8, "sf", 3)
+    _contig(sf, "sf")
+    if tuple(sf.shape) != shape:
+        raise ValueError(f"sf must be {shape}")
+    _same_device(scales, sf=sf)
+    _check(lib.dq_fp4_tile_scales(_ptr(scales), R, K, code, _ptr(sf), _stream(stream)), "dq_fp4_tile_scales")
+    return sf
+
+
+def _fp4_operand(q, sf, s, code, name):
+    _need(q, torch.uint8, name, 2)
+    _contig(q, name)
+    R, K = q.shape[0], q.shape[1] * 2
+    _need(sf, torch.uint8, f"{name} scales", 3)
+    _contig(sf, f"{name} scales")
+    if tuple(sf.shape) != _fp4_scale_shape(R, K, code):
+        raise ValueError(f"{name} scales: expected {_fp4_scale_shape(R, K, code)}, got {tuple(sf.shape)}")
+    if s is not None:
+        _need(s, torch.float32, f"{name} row scales", 1)
+        _contig(s, f"{name} row scales")
+        if s.numel() != R:
+            raise ValueError(f"{name} row scales: expected {R}, got {s.numel()}")
+    return R, K
+
+
+def dq_fp4_dequantize(q, sf, s=None, fmt="nv", out=None, stream=None) -> torch.Tensor:
+    """The values 4-bit codes stand for: bf16 [rows, K] = e2m1 * block scale * s
+    (s fp32 [rows] or None)."""
+    code = _fp4_fmt(fmt)
+    M, K = _fp4_operand(q, sf, s, code, "q")
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, "out", 2)
+    _contig(out, "out")
+    if tuple(out.shape) != (M, K):
+        raise ValueError(f"out must be {(M, K)}")
+    _same_device(q, sf=sf, s=s, out=out)
+    _check(lib.dq_fp4_dequantize(_ptr(q), _ptr(sf), _ptr(s), M, K, code, _ptr(out), _stream(stream)),
+           "dq_fp4_dequantize")
+    return out
+
+
+def dq_fp4_linear(A, sfa, s_row, W, sfw, s_col, bias=None, fmt="nv", out=None, out_dtype="bf16", stream=None):
+    """out[M, N] = bf16(acc * s_row * s_col + bias) from 4-bit operands: A uint8
+    [M, K/2] and W uint8 [N, K/2] with their tiled block scales, acc the
+    block-scaled product on the tensor cores (or acc itself with
+    out_dtype="f32").  s_row / s_col may be None (1)."""
+    code = _fp4_fmt(fmt)
+    if out_dtype in ("f32", "float32", torch.float32, DQ_OUT_F32):
+        oc, odt = DQ_OUT_F32, torch.float32
+    elif out_dtype in ("bf16", torch.bfloat16, DQ_OUT_BF16):
+        oc, odt = DQ_OUT_BF16, torch.bfloat16
+    else:
+        raise ValueError(f"out_dtype {out_dtype!r}")
+    M, K = _fp4_operand(A, sfa, s_row, code, "A")
+    N, KW = _fp4_operand(W, sfw, s_col, code, "W")
+    if K != KW:
+        raise ValueError("A and W disagree on K")
+    if bias is not None:
+        _need(bias, torch.bfloat16, "bias", 1)
+        _contig(bias, "bias")
+        if bias.numel() != N:
+            raise ValueError("bias length mismatch")
+    if out is None:
+        out = torch.empty((M, N), dtype=odt, device=A.device)
+    _need(out, odt, "out", 2)
+    _contig(out, "out")
+    if tuple(out.shape) != (M, N):
+        raise ValueError(f"out: expected shape {(M, N)}, got {tuple(out.shape)}")
+    _same_device(A, sfa=sfa, s_row=s_row, W=W, sfw=sfw, s_col=s_col, bias=bias, out=out)
+    _check(lib.dq_fp4_linear(_ptr(A), _ptr(sfa), _ptr(s_row), M, K, _ptr(W), _ptr(sfw), _ptr(s_col), N, code,
+                             _ptr(bias), _ptr(out), oc, _stream(stream)), "dq_fp4_linear")
+    return out
+
+
+# ---------------------------------------------------------------- 8-bit checkpoints
+
+def _act8_shapes(M: int, K: int):
+    g = (M + 31) // 32
+    return (2 * g, K, 16), (g, K)
+
+
+def _act8_operand(codes, scales, M: int):
+    _need(codes, torch.int8, "codes", 3)
+    _need(scales, torch.uint8, "scales", 2)
+    _contig(codes, "codes")
+    _contig(scales, "scales")
+    K = scales.shape[1]
+    want = _act8_shapes(M, K)
+    if tuple(codes.shape) != want[0] or tuple(scales.shape) != want[1]:
+        raise ValueError(f"{M} tokens of {K} features need codes {want[0]} and scales {want[1]}")
+    return K
+
+
+def dq_act8_pack(x: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor = None, stream=None):
+    """An activation kept in 8 bits: x bf16 [M, K] (K % 16 == 0) -> (codes int8
+    [2 ceil(M/32), K, 16], scales uint8 [ceil(M/32), K]); blocks of 32 tokens
+    of one feature share a power-of-two scale."""
+    _need(x, torch.bfloat16, "x", 2)
+    ld = _rows(x, "x")
+    M, K = x.shape
+    if K < 1 or K % 16 != 0:
+        raise ValueError(f"x: the row length must be a positive multiple of 16, got {K}")
+    cs, ss = _act8_shapes(M, K)
+    if codes is None:
+        codes = torch.empty(cs, dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty(ss, dtype=torch.uint8, device=x.device)
+    if _act8_operand(codes, scales, M) != K:
+        raise ValueError("codes and scales do not match x")
+    _same_device(x, codes=codes, scales=scales)
+    _check(lib.dq_act8_pack(_ptr(x), M, K, ld, _ptr(codes), _ptr(scales), _stream(stream)), "dq_act8_pack")
+    return codes, scales
+
+
+def dq_act8_unpack(codes, scales, M: int, out=None, stream=None) -> torch.Tensor:
+    """The bf16 [M, K] values of an 8-bit checkpoint (exact)."""
+    K = _act8_operand(codes, scales, M)
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
+    _need(out, torch.bfloat16, "out", 2)
+    _contig(out, "out")
+    if tuple(out.shape) != (M, K):
+        raise ValueError(f"out must be {(M, K)}")
+    _same_device(codes, scales=scales, out=out)
+    _check(lib.dq_act8_unpack(_ptr(codes), _ptr(scales), M, K, _ptr(out), _stream(stream)), "dq_act8_unpack")
     return out
 
 

@@ -1,0 +1,765 @@
+// fp4.cu -- the microscaled 4-bit linear layer's product: e2m1 codes with
+// block scales on both sides (fp4_quant.cu describes the formats),
+//     acc[m, n] = sum over blocks b of sfa[m, b] sfw[n, b] sum_{k in b} a[m, k] w[n, k]
+//     out = bf16(((acc * s_row[m]) * s_col[n]) + bias[n])
+// on tcgen05.mma kind::mxf4nvf4.block_scale: the tensor core applies the block
+// scales itself, out of tensor memory, and accumulates in fp32.
+//
+// Operand layout: codes K-major, 256 features (128 bytes, 128B-swizzled) per
+// pipeline stage, four MMAs of K = 64 each.  Block scales arrive as the
+// 512-byte tiles the quantizer writes (128 rows x 4 blocks: byte 16 (r % 32) +
+// 4 (r / 32) + b), which one tcgen05.cp.32x128b.warpx4 puts into four columns
+// of tensor memory as the MMA wants them (column r / 32, lane r % 32,
+// replicated to the four sub-partitions); a tile serves one MMA (NV) or two
+// (MX, selected by the descriptor's scale id).
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "fp4.h"
+#include "gemm_common.cuh"
+#include "internal.h"
+#include "pipeline.cuh"
+#include "sm100.cuh"
+
+namespace dq {
+namespace {
+
+constexpr int F4_KB = 128;           // code bytes per row and stage (256 features)
+constexpr int F4_KE = 256;           // features per stage
+
+// Scale tiles per stage (per 128 rows): NV 4 (64 features each), MX 2 (128).
+__host__ __device__ constexpr int f4_tiles(bool nv) { return nv ? 4 : 2; }
+
+// Instruction descriptor for kind::mxf4nvf4 with e2m1 A and B, both K-major:
+// scale type (0 ue4m3, 1 ue8m0) at bit 23, A / B scale ids at 29 / 4 (which
+// half of the four scale bytes a block-32 MMA takes: 0 or 2).
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool nv, int half) {
+  return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (nv ? 0u : 1u << 23) |
+         (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(2 * half) << 29) |
+         (static_cast<uint32_t>(2 * half) << 4);
+}
+
+// Shared-memory descriptor of one 512-byte scale tile: 32 rows of 16 bytes, no
+// swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sf_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 16) |
+         (static_cast<uint64_t>(128u >> 4) << 32) | (1ull << 46);
+}
+
+template <int CG>
+__device__ __forceinline__ void cp_sf(uint32_t taddr, uint64_t desc) {
+  if constexpr (CG == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <int CG, bool NV>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+#define DQ_FP4_MMA(CGS, VEC)                                                                               \
+  asm volatile(                                                                                            \
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                    \
+      "tcgen05.mma.cta_group::" CGS ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                          \
+      " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                                   \
+      "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                                    \
+      : "memory")
+  if constexpr (CG == 1 && NV) DQ_FP4_MMA("1", "4X");
+  else if constexpr (CG == 1) DQ_FP4_MMA("1", "2X");
+  else if constexpr (NV) DQ_FP4_MMA("2", "4X");
+  else DQ_FP4_MMA("2", "2X");
+#undef DQ_FP4_MMA
+}
+
+// ---------------------------------------------------------------- few tokens
+// The weight stream is the bound (0.53 - 0.56 bytes per weight at HBM rate),
+// so the weight's 128 channels sit on the MMA's M and the tokens on its N, one
+// work unit per CTA, several CTAs per SM: their loads overlap each other's
+// prologue, pipeline ends and epilogue.  Few channel tiles: the features are
+// split over a cluster of up to 8 CTAs, whose fp32 partial tiles are added
+// through distributed shared memory in split order.
+//   warp 0 producer, warp 1 scale copies and MMAs, all six warps the epilogue.
+constexpr int FS_THREADS = 192;
+constexpr int FS_MAX_STAGES = 8;
+constexpr int FS_BAR_BYTES = 256;
+
+struct FewArgs {
+  int M, N;
+  int ks_total;            // 64-feature MMA steps: ceil(K / 64)
+  int kb_total;            // stages: ceil(K / 256)
+  int bn;                  // tokens per tile (multiple of 16, <= 128)
+  int nt, tt, splits;      // channel tiles, token tiles, feature splits
+  int stages;
+  int tmem_cols, sf_col;   // allocation; first column of the scale slots
+  int sf_slots;            // tensor-memory scale slots
+  uint32_t off_bar;
+  const float* s_row;
+  const float* s_col;
+  const uint16_t* bias;
+  void* out;
+  int raw;                 // fp32 accumulators instead of bf16
+  WaitCtl wait;
+};
+
+template <bool NV>
+__global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_constant__ CUtensorMap tm_w,
+                                                             const __grid_constant__ CUtensorMap tm_x,
+                                                             const __grid_constant__ CUtensorMap tm_sw,
+                                                             const __grid_constant__ CUtensorMap tm_sx,
+                                                             const FewArgs g) {
+  constexpr int T = f4_tiles(NV);
+  constexpr uint32_t W_BYTES = 128 * F4_KB;
+  constexpr uint32_t S_BYTES = T * 512;
+  constexpr int SF_COLS = 2 * T * 4;                 // A and B scale columns per stage
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - raw);
+  // stage: weight codes, token codes, weight scales, token scales
+  const uint32_t x_bytes = static_cast<uint32_t>(g.bn) * F4_KB;
+  const uint32_t stage_bytes = W_BYTES + x_bytes + 2 * S_BYTES;   // a multiple of 1024 (bn % 8 == 0)
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + g.off_bar);
+  uint64_t* const empty = full + FS_MAX_STAGES;
+  uint64_t* const accf = empty + FS_MAX_STAGES;
+  uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(accf + 1);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < g.stages; ++i) {
+      mbar_init(smem_u32(full + i), 1);
+      mbar_init(smem_u32(empty + i), 1);
+    }
+    mbar_init(smem_u32(accf), 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_sw);
+    tma_prefetch_desc(&tm_sx);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_holder), static_cast<uint32_t>(g.tmem_cols));
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // unit: (channel tile, token tile, split), splits neighbouring (one cluster)
+  const int u = blockIdx.x;
+  const int split = u % g.splits;
+  const int tile = u / g.splits;
+  const int nt = tile / g.tt;
+  const int tt = tile - nt * g.tt;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(split) * g.kb_total / g.splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(split + 1) * g.kb_total / g.splits);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!pipe::wait(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) break;
+        const uint32_t fb = smem_u32(full + stage);
+        const uint32_t sw = base + static_cast<uint32_t>(stage) * stage_bytes;
+        mbar_arrive_expect_tx(fb, stage_bytes);
+        tma_load_2d(sw, &tm_w, fb, kb * F4_KB, nt * 128);
+        tma_load_2d(sw + W_BYTES + x_bytes, &tm_sw, fb, kb * T * 64, nt);
+        tma_load_2d(sw + W_BYTES, &tm_x, fb, kb * F4_KB, tt * g.bn);
+        tma_load_2d(sw + W_BYTES + x_bytes + S_BYTES, &tm_sx, fb, kb * T * 64, tt * g.bn / 128);
+        ++issued;
+        if (++stage == g.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // every copy issued lands before the CTA can exit
+      volatile int never = 0;
+      for (int i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
+        pipe::wait(smem_u32(full + i % g.stages), static_cast<uint32_t>((i / g.stages) & 1), g.wait, &never);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const uint32_t col_x = static_cast<uint32_t>(((tt * g.bn) % 128) / 32);   // first token's scale column
+      for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+        if (!pipe::wait(smem_u32(full + stage), phase, g.wait, abort_flag)) break;
+        // the scale slot's previous user must have completed
+        if (i >= g.sf_slots) {
+          const int j = i - g.sf_slots;
+          if (!pipe::wait(smem_u32(empty + j % g.stages), static_cast<uint32_t>((j / g.stages) & 1), g.wait, abort_flag))
+            break;
+        }
+        tc_fence_after();
+        const uint32_t sw = base + static_cast<uint32_t>(stage) * stage_bytes;
+        const uint32_t sfa = tmem + static_cast<uint32_t>(g.sf_col + (i % g.sf_slots) * SF_COLS);
+        const uint32_t sfb = sfa + T * 4;
+        const int steps = min(4, g.ks_total - 4 * kb);
+        const uint64_t da = sf_desc(sw + W_BYTES + x_bytes), db = sf_desc(sw + W_BYTES + x_bytes + S_BYTES);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          cp_sf<1>(sfa + 4 * t, da + 32 * t);
+          cp_sf<1>(sfb + 4 * t, db + 32 * t);
+        }
+        const uint64_t ad = smem_desc_kmajor<128>(sw);
+        const uint64_t bd = smem_desc_kmajor<128>(sw + W_BYTES);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < steps) {
+            const int t = NV ? k : k >> 1;
+            mma_fp4<1, NV>(tmem, ad + 2 * k, bd + 2 * k, idesc_fp4(128, g.bn, NV, NV ? 0 : k & 1), sfa + 4 * t,
+                           sfb + 4 * t + col_x, (i > 0 || k > 0) ? 1u : 0u);
+          }
+        mma_commit(smem_u32(empty + stage));
+        if (++stage == g.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // every MMA issued has completed once this flips
+      mma_commit(smem_u32(accf));
+      volatile int never = 0;
+      pipe::wait(smem_u32(accf), 0, g.wait, &never);
+    }
+  }
+  __syncwarp();
+  // ------------------------------------------------------------ epilogue
+  // The accumulator goes to shared memory as [token][channel] fp32 (the
+  // consumed stage ring), from where the split's CTAs add their shares.
+  const bool ok = pipe::wait(smem_u32(accf), 0, g.wait, abort_flag);
+  tc_fence_after();
+  if (warp >= 2 && __all_sync(0xffffffffu, ok)) {
+    const int q = warp & 3;
+    const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    for (int c0 = 0; c0 < g.bn; c0 += 16) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(tb + c0, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        pipe::sts32(base + static_cast<uint32_t>((c0 + j) * 128 + q * 32 + lane) * 4u, r[j]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, static_cast<uint32_t>(g.tmem_cols));
+  if (g.splits > 1) cluster_sync_all();
+  const int rows = (g.bn + g.splits - 1) / g.splits;
+  const int r0 = split * rows;
+  const int r1 = min(g.bn, r0 + rows);
+  for (int i = threadIdx.x; i < (r1 - r0) * 32; i += FS_THREADS) {
+    const int tok = r0 + (i >> 5);
+    const int quad = i & 31;
+    const int m = tt * g.bn + tok;
+    const int ch = nt * 128 + 4 * quad;
+    if (m >= g.M || ch >= g.N) continue;              // N % 8 == 0: the quad is all in or all out
+    const uint32_t off = base + static_cast<uint32_t>(tok * 128 + 4 * quad) * 4u;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (g.splits > 1) {
+      for (int sp = 0; sp < g.splits; ++sp) {
+        const float4 v = ld_shared_cluster_f4(map_to_rank(off, static_cast<uint32_t>(sp)));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+    } else {
+      const uint4 v = pipe::lds128(off);
+      s = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    const int64_t o = static_cast<int64_t>(m) * g.N + ch;
+    if (g.raw) {
+      *reinterpret_cast<float4*>(static_cast<float*>(g.out) + o) = s;
+      continue;
+    }
+    const float sr = g.s_row != nullptr ? __ldg(g.s_row + m) : 1.0f;
+    float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (g.s_col != nullptr) sc = __ldg(reinterpret_cast<const float4*>(g.s_col + ch));
+    float y[4] = {__fmul_rn(__fmul_rn(s.x, sr), sc.x), __fmul_rn(__fmul_rn(s.y, sr), sc.y),
+                  __fmul_rn(__fmul_rn(s.z, sr), sc.z), __fmul_rn(__fmul_rn(s.w, sr), sc.w)};
+    if (g.bias != nullptr) {
+      const uint2 b = __ldg(reinterpret_cast<const uint2*>(g.bias + ch));
+      y[0] = __fadd_rn(y[0], __uint_as_float(b.x << 16));
+      y[1] = __fadd_rn(y[1], __uint_as_float(b.x & 0xffff0000u));
+      y[2] = __fadd_rn(y[2], __uint_as_float(b.y << 16));
+      y[3] = __fadd_rn(y[3], __uint_as_float(b.y & 0xffff0000u));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + o) =
+        make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  }
+  if (g.splits > 1) cluster_sync_all();               // peers have read this CTA's partials
+}
+
+// ---------------------------------------------------------------- many tokens
+// A pair of SMs per 256 x BN tile (cta_group::2), as the int8 pair kernel:
+// each CTA loads its 128 token rows and half of the tile's weight rows, plus
+// its own rows' scale tiles and ALL of the tile's weight scale tiles (each
+// SM's tensor core multiplies its rows with every column, so both tensor
+// memories need every column's scales).
+//   warp 0 producer, warp 1 (leader) scale copies and MMAs, warps 2..9
+//   epilogue, two per TMEM sub-partition on alternate 32-column chunks.
+template <int BN, bool NV>
+struct CfgP {
+  static constexpr int T = f4_tiles(NV);
+  static constexpr int RB = (BN + 127) / 128;           // weight scale row blocks of a tile
+  static constexpr int A_BYTES = 128 * F4_KB;
+  static constexpr int B_BYTES = (BN / 2) * F4_KB;
+  static constexpr int SA_BYTES = T * 512;
+  static constexpr int SB_BYTES = RB * T * 512;
+  static constexpr int CTA_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int OUT_BUF_BYTES = 32 * 32 * 4;
+  static constexpr int OUT_BYTES = EPI_WARPS * OUT_BUF_BYTES;
+  static constexpr int BAR_BYTES = 512;
+  static constexpr int SLACK = 1024;
+  static constexpr int STAGES = (227 * 1024 - SLACK - BAR_BYTES - OUT_BYTES - kScSlotBytes) / CTA_BYTES;
+  static constexpr int ACC_BUFS = BN <= 192 ? 2 : 1;
+  static constexpr int SF_A = T * 4, SF_B = T * RB * 4; // scale columns per stage
+  static constexpr int SF_COLS = SF_A + SF_B;
+  static constexpr int SF_COL0 = ACC_BUFS * BN;
+  static constexpr int SLOTS_FIT = (512 - SF_COL0) / SF_COLS;
+  static constexpr int SLOTS = SLOTS_FIT < STAGES ? SLOTS_FIT : STAGES;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int OFF_SA = STAGES * (A_BYTES + B_BYTES);
+  static constexpr int OFF_SB = OFF_SA + STAGES * SA_BYTES;
+  static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;
+  static constexpr int OFF_SC = OFF_OUT + OUT_BYTES;
+  static constexpr int OFF_BARS = OFF_SC + kScSlotBytes;
+  static constexpr int SMEM_BYTES = OFF_BARS + BAR_BYTES + SLACK;
+  static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= 227 * 1024, "resources");
+  static_assert((2 * STAGES + 2 * ACC_BUFS + 3) * 8 + 8 <= BAR_BYTES, "barrier area");
+  static_assert(BN % 64 == 0 && BN <= 256, "tile width: a scale row block or half of one");
+};
+
+template <int BN, bool NV>
+__global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
+                    const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ GemmArgs g) {
+  using C = CfgP<BN, NV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sA = smem_u32(smem);
+  const uint32_t sB = sA + C::STAGES * C::A_BYTES;
+  const uint32_t sSA = sA + C::OFF_SA;
+  const uint32_t sSB = sA + C::OFF_SB;
+  uint8_t* sOut = smem + C::OFF_OUT;
+  const uint32_t sc_slot = sA + C::OFF_SC;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+  uint64_t* empty_bar = full_bar + C::STAGES;
+  uint64_t* accf_bar = empty_bar + C::STAGES;
+  uint64_t* acce_bar = accf_bar + C::ACC_BUFS;
+  uint64_t* drain_bar = acce_bar + C::ACC_BUFS;
+  uint64_t* sc_full = drain_bar + 1;
+  uint64_t* sc_free = sc_full + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sc_free + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int G = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(smem_u32(full_bar + s), 1);
+      mbar_init(smem_u32(empty_bar + s), 1);
+    }
+    for (int a = 0; a < C::ACC_BUFS; ++a) {
+      mbar_init(smem_u32(accf_bar + a), 1);
+      mbar_init(smem_u32(acce_bar + a), 2 * C::EPI_WARPS);
+    }
+    mbar_init(smem_u32(drain_bar), 1);
+    mbar_init(smem_u32(sc_full), 1);
+    mbar_init(smem_u32(sc_free), C::EPI_WARPS);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_sa);
+    tma_prefetch_desc(&tm_sb);
+    tma_prefetch_desc(&tm_c);
+  }
+  // no column scales (MX): the slot holds ones for the whole launch
+  if (g.s_col == nullptr)
+    for (int i = threadIdx.x; i < 256; i += C::THREADS) pipe::sts32(sc_slot + 4u * i, __float_as_uint(1.0f));
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_holder), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < g.num_tiles; t += G) {
+        const int ta = t / g.b_tiles;
+        const int n0 = (t - ta * g.b_tiles) * BN;
+        for (int kb = 0; kb < g.kb_total; ++kb) {
+          if (!mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, g.wait, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(full_bar + stage);
+          if (leader) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
+          const uint32_t fbl = map_to_rank(fb, 0);
+          tma_load_2d_pair(sA + stage * C::A_BYTES, &tm_a, fbl, kb * F4_KB, ta * 256 + static_cast<int>(rank) * 128);
+          tma_load_2d_pair(sB + stage * C::B_BYTES, &tm_b, fbl, kb * F4_KB, n0 + static_cast<int>(rank) * (BN / 2));
+          tma_load_2d_pair(sSA + stage * C::SA_BYTES, &tm_sa, fbl, kb * C::T * 64, ta * 2 + static_cast<int>(rank));
+          tma_load_2d_pair(sSB + stage * C::SB_BYTES, &tm_sb, fbl, kb * C::T * 64, n0 / 128);
+          ++issued;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        // Loads already issued land before the CTA leaves (see gemm2sm.cu).
+        if (leader) {
+          WaitCtl quick = g.wait;
+          quick.timeout_ns = quick.timeout_ns < 50000000ull ? quick.timeout_ns : 50000000ull;
+          volatile int never = 0;
+          for (long long i = 0; i < issued && i < C::STAGES; ++i) {
+            if (--stage < 0) {
+              stage = C::STAGES - 1;
+              phase ^= 1;
+            }
+            mbar_wait(smem_u32(full_bar + stage), phase, quick, &never);
+          }
+        } else {
+          const uint64_t t0 = globaltimer();
+          while (globaltimer() - t0 < 100000ull) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (leader && lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      long long it = 0;
+      bool ok = true;
+      const int ks_total = (g.K + 63) / 64;
+      for (int t = pair; ok && t < g.num_tiles; t += G) {
+        // an odd tile of width 192 (or 64) starts in the middle of a scale row block
+        const uint32_t col_b = static_cast<uint32_t>((((t % g.b_tiles) * BN) % 128) / 32);
+        if (!mbar_wait(smem_u32(acce_bar + acc), acc_phase ^ 1, g.wait, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
+        for (int kb = 0; kb < g.kb_total; ++kb, ++it) {
+          if (!mbar_wait(smem_u32(full_bar + stage), phase, g.wait, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (C::SLOTS < C::STAGES && it >= C::SLOTS) {   // the scale slot's previous user has completed
+            const long long j = it - C::SLOTS;
+            if (!mbar_wait(smem_u32(empty_bar + j % C::STAGES), static_cast<uint32_t>((j / C::STAGES) & 1), g.wait,
+                           abort_flag)) {
+              ok = false;
+              break;
+            }
+          }
+          tc_fence_after();
+          const uint32_t sfa = tmem_base + C::SF_COL0 + static_cast<uint32_t>(it % C::SLOTS) * C::SF_COLS;
+          const uint32_t sfb = sfa + C::SF_A;
+          const uint64_t da = sf_desc(sSA + stage * C::SA_BYTES), db = sf_desc(sSB + stage * C::SB_BYTES);
+#pragma unroll
+          for (int s = 0; s < C::T; ++s) {
+            cp_sf<2>(sfa + 4 * s, da + 32 * s);
+#pragma unroll
+            for (int r = 0; r < C::RB; ++r) cp_sf<2>(sfb + 4 * (s * C::RB + r), db + 32 * (r * C::T + s));
+          }
+          const uint64_t ad = smem_desc_kmajor<128>(sA + stage * C::A_BYTES);
+          const uint64_t bd = smem_desc_kmajor<128>(sB + stage * C::B_BYTES);
+          const int steps = min(4, ks_total - 4 * kb);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) {
+              const int s = NV ? k : k >> 1;
+              mma_fp4<2, NV>(d, ad + 2 * k, bd + 2 * k, idesc_fp4(256, BN, NV, NV ? 0 : k & 1), sfa + 4 * s,
+                             sfb + 4 * C::RB * s + col_b, (kb > 0 || k > 0) ? 1u : 0u);
+            }
+          mma_commit_pair_both(smem_u32(empty_bar + stage));
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_both(smem_u32(accf_bar + acc));
+        if (++acc == C::ACC_BUFS) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      mma_commit_pair(map_to_rank(smem_u32(drain_bar), 0));
+      volatile int never = 0;
+      mbar_wait(smem_u32(drain_bar), 0, g.wait, &never);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    constexpr int GROUPS = C::EPI_WARPS / 4;
+    const int ew = warp - 2;
+    const int sp = warp & 3;
+    const int grp = ew / 4;
+    const int ep_tid = threadIdx.x - 64;
+    uint8_t* my_out = sOut + ew * C::OUT_BUF_BYTES;
+    int out_flip = 0;
+    auto next_buf = [&]() -> uint8_t* {
+      if (g.out_s32) {
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        return my_out;
+      }
+      if (lane == 0) bulk_wait_group_read<1>();
+      __syncwarp();
+      uint8_t* b = my_out + out_flip * (C::OUT_BUF_BYTES / 2);
+      out_flip ^= 1;
+      return b;
+    };
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    uint32_t sc_phase = 0;
+    for (int t = pair; t < g.num_tiles; t += G) {
+      const int ta = t / g.b_tiles;
+      const int n0 = (t - ta * g.b_tiles) * BN;
+      const int m_slab = ta * 256 + static_cast<int>(rank) * 128 + sp * 32;
+      const int m = m_slab + lane;
+      if (ep_tid == 0) {
+        if (t != pair && !mbar_wait(smem_u32(sc_free), sc_phase ^ 1, g.wait, abort_flag)) break;
+        // the tile's column scales (unless there are none) and bias
+        const int ncols = min(BN, g.N - n0);
+        const uint32_t sb = !g.out_s32 && g.s_col != nullptr ? static_cast<uint32_t>(ncols) * 4u : 0u;
+        const uint32_t bb = !g.out_s32 && g.bias != nullptr ? static_cast<uint32_t>(ncols) * 2u : 0u;
+        mbar_arrive_expect_tx(smem_u32(sc_full), sb + bb);
+        if (sb) bulk_load_1d(sc_slot, g.s_col + n0, sb, smem_u32(sc_full));
+        if (bb) bulk_load_1d(sc_slot + kScBiasOff, g.bias + n0, bb, smem_u32(sc_full));
+      }
+      const float srow = (!g.out_s32 && g.s_row != nullptr && m < g.M) ? __ldg(g.s_row + m) : 1.0f;
+      if (!mbar_wait(smem_u32(accf_bar + acc), acc_phase, g.wait, abort_flag)) break;
+      if (!mbar_wait(smem_u32(sc_full), sc_phase, g.wait, abort_flag)) break;
+      sc_phase ^= 1;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(sp * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      constexpr int NCH = BN / 32;
+      const int last_c = grp + ((NCH - 1 - grp) / GROUPS) * GROUPS;
+#pragma unroll 1
+      for (int c0 = grp; c0 < NCH; c0 += 2 * GROUPS) {
+        uint32_t r[2][32];
+        const bool two = c0 + GROUPS < NCH;
+        tmem_ld_32x32b_x32(tbase + c0 * 32, r[0]);
+        if (two) tmem_ld_32x32b_x32(tbase + (c0 + GROUPS) * 32, r[1]);
+        tmem_ld_wait();
+        if (c0 == last_c || (two && c0 + GROUPS == last_c)) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(acce_bar + acc), 0));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = c0 + i * GROUPS;
+          if (i == 1 && !two) break;
+          store_row_chunk_staged<true>(g, &tm_c, next_buf(), lane, m_slab, n0 + c * 32, r[i], srow, sc_slot, c * 32);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(sc_free));
+      if (++acc == C::ACC_BUFS) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+// ---------------------------------------------------------------- host
+
+// Scale tiles [row blocks][tiles x 512 B] as 8-byte elements, box one stage
+// (64 elements per tile) x `box_rows` row blocks; zero fill past the end.
+dq_status make_tmap_sf(CUtensorMap* map, const uint8_t* sf, int64_t row_blocks, int64_t atoms, int tiles, int box_rows) {
+  return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, sf, static_cast<uint64_t>(atoms) * 64,
+                      static_cast<uint64_t>(row_blocks), static_cast<uint64_t>(atoms) * 512,
+                      static_cast<uint32_t>(tiles) * 64, static_cast<uint32_t>(box_rows), 0);
+}
+
+template <bool NV>
+dq_status launch_few(const uint8_t* A, const uint8_t* sfa, int64_t M, int64_t K, const uint8_t* W, const uint8_t* sfw,
+                     int64_t N, FewArgs g, int sm_count, cudaStream_t stream) {
+  constexpr int T = f4_tiles(NV);
+  const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
+  g.bn = M >= 128 ? 128 : static_cast<int>((M + 15) / 16 * 16);
+  g.tt = static_cast<int>((M + g.bn - 1) / g.bn);
+  g.nt = static_cast<int>((N + 127) / 128);
+  g.kb_total = static_cast<int>((K + F4_KE - 1) / F4_KE);
+  g.ks_total = static_cast<int>((K + 63) / 64);
+  // As many CTAs per SM as three (two from 64 tokens): the smallest split that
+  // gives every slot a unit, as long as a unit keeps two stages of features.
+  const int per_sm = g.bn <= 48 ? 3 : 2;
+  const int64_t tiles = static_cast<int64_t>(g.nt) * g.tt;
+  g.splits = 1;
+  while (g.splits < 8 && tiles * g.splits < static_cast<int64_t>(per_sm) * sm_count && g.kb_total / (2 * g.splits) >= 2)
+    g.splits *= 2;
+  const int stage_bytes = 128 * F4_KB + g.bn * F4_KB + 2 * T * 512;
+  const int limit = (227 * 1024 - per_sm * 1024) / per_sm;
+  g.stages = (limit - 1024 - FS_BAR_BYTES) / stage_bytes;
+  const int max_need = (g.kb_total + g.splits - 1) / g.splits;
+  g.stages = std::min({g.stages, FS_MAX_STAGES, max_need});
+  // the fp32 tile reuses the ring
+  const int ring = std::max(g.stages * stage_bytes, g.bn * 512);
+  g.off_bar = static_cast<uint32_t>((ring + 15) / 16 * 16);
+  const int smem = static_cast<int>(g.off_bar) + FS_BAR_BYTES + 1024;
+  constexpr int SF_COLS = 2 * T * 4;
+  g.sf_col = g.bn <= 32 ? 32 : g.bn <= 64 ? 64 : 128;
+  g.tmem_cols = g.sf_col == 128 ? 256 : 128;
+  g.sf_slots = std::min((g.tmem_cols - g.sf_col) / SF_COLS, g.stages);
+  CUtensorMap tw, tx, tsw, tsx;
+  dq_status st;
+  if ((st = make_tmap_u8_2d(&tw, W, K / 2, N, K / 2, F4_KB, 128, 128)) != DQ_OK) return st;
+  if ((st = make_tmap_u8_2d(&tx, A, K / 2, M, K / 2, F4_KB, g.bn, 128)) != DQ_OK) return st;
+  if ((st = make_tmap_sf(&tsw, sfw, (N + 127) / 128, atoms, T, 1)) != DQ_OK) return st;
+  if ((st = make_tmap_sf(&tsx, sfa, (M + 127) / 128, atoms, T, 1)) != DQ_OK) return st;
+  auto k = fp4_few_kernel<NV>;
+  if ((st = smem_limit_once(reinterpret_cast<const void*>(k), smem)) != DQ_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.splits));
+  cfg.blockDim = dim3(FS_THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(g.splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = g.splits > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, tw, tx, tsw, tsx, g);
+  return e == cudaSuccess ? DQ_OK : cuda_fail(e);
+}
+
+template <int BN, bool NV>
+dq_status launch_pair(const uint8_t* A, const uint8_t* sfa, const uint8_t* W, const uint8_t* sfw, GemmArgs g, int pairs,
+                      cudaStream_t stream) {
+  using C = CfgP<BN, NV>;
+  const int64_t K = g.K;
+  const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
+  g.a_tiles = (g.M + 255) / 256;
+  g.b_tiles = (g.N + BN - 1) / BN;
+  g.kb_total = static_cast<int>((K + F4_KE - 1) / F4_KE);
+  const int64_t tiles = static_cast<int64_t>(g.a_tiles) * g.b_tiles;
+  if (tiles > 0x3fffffff) return DQ_ERR_UNSUPPORTED;
+  g.num_tiles = static_cast<int>(tiles);
+  CUtensorMap ta, tb, tsa, tsb, tc;
+  dq_status st;
+  if ((st = make_tmap_u8_2d(&ta, A, K / 2, g.M, K / 2, F4_KB, 128, 128)) != DQ_OK) return st;
+  if ((st = make_tmap_u8_2d(&tb, W, K / 2, g.N, K / 2, F4_KB, BN / 2, 128)) != DQ_OK) return st;
+  if ((st = make_tmap_sf(&tsa, sfa, (g.M + 127) / 128, atoms, C::T, 1)) != DQ_OK) return st;
+  if ((st = make_tmap_sf(&tsb, sfw, (g.N + 127) / 128, atoms, C::T, C::RB)) != DQ_OK) return st;
+  if ((st = make_tmap_out_2d(&tc, g.out, g.N, g.M, g.out_s32 ? 4 : 2)) != DQ_OK) return st;
+  auto k = fp4_pair_kernel<BN, NV>;
+  if ((st = smem_limit_once(reinterpret_cast<const void*>(k), C::SMEM_BYTES)) != DQ_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(pairs, tiles)));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ta, tb, tsa, tsb, tc, g);
+  return e == cudaSuccess ? DQ_OK : cuda_fail(e);
+}
+
+}  // namespace
+}  // namespace dq
+
+using namespace dq;
+
+extern "C" {
+
+dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float* s_row, int64_t M, int64_t K,
+                        const uint8_t* W, const uint8_t* sfw, const float* s_col, int64_t N, int fmt,
+                        const void* bias_bf16, void* out, dq_out_dtype out_dtype, dq_stream_t stream) {
+  if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || M < 0 || N < 1 || K < 1) return DQ_ERR_INVALID_ARG;
+  if (out_dtype != DQ_OUT_BF16 && out_dtype != DQ_OUT_F32) return DQ_ERR_INVALID_ARG;
+  if (W == nullptr || sfw == nullptr || (M > 0 && (A == nullptr || sfa == nullptr || out == nullptr)))
+    return DQ_ERR_INVALID_ARG;
+  if (K % 32 != 0 || N % 8 != 0 || M > kFp4MaxDim || N > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (!aligned(A, 16) || !aligned(sfa, 16) || !aligned(W, 16) || !aligned(sfw, 16) || !aligned(out, 16) ||
+      !aligned(s_row, 4) || !aligned(s_col, 16) || !aligned(bias_bf16, 16))
+    return DQ_ERR_UNSUPPORTED;
+  DeviceInfo* d = nullptr;
+  dq_status st = current_device(&d);
+  if (st != DQ_OK) return st;
+  if (M == 0) return DQ_OK;
+  const auto cs = reinterpret_cast<cudaStream_t>(stream);
+  const bool nv = fmt == DQ_FP4_NV;
+  const WaitCtl wait{d->err_word, wait_timeout_ns()};
+  if (M <= 256) {
+    FewArgs f = {};
+    f.M = static_cast<int>(M);
+    f.N = static_cast<int>(N);
+    f.s_row = s_row;
+    f.s_col = s_col;
+    f.bias = static_cast<const uint16_t*>(bias_bf16);
+    f.out = out;
+    f.raw = out_dtype == DQ_OUT_F32;
+    f.wait = wait;
+    return nv ? launch_few<true>(A, sfa, M, K, W, sfw, N, f, d->sm_count, cs)
+              : launch_few<false>(A, sfa, M, K, W, sfw, N, f, d->sm_count, cs);
+  }
+  GemmArgs g = {};
+  g.M = static_cast<int>(M);
+  g.N = static_cast<int>(N);
+  g.K = static_cast<int>(K);
+  g.s_row = s_row;
+  g.s_col = s_col;
+  g.bias = static_cast<const uint16_t*>(bias_bf16);
+  g.out = out;
+  g.out_s32 = out_dtype == DQ_OUT_F32;
+  g.wait = wait;
+  int pairs = 0;
+  if ((st = pair_slots(*d, &pairs)) != DQ_OK) return st;
+  return nv ? launch_pair<192, true>(A, sfa, W, sfw, g, pairs, cs) : launch_pair<192, false>(A, sfa, W, sfw, g, pairs, cs);
+}
+
+}  // extern "C"

@@ -1,0 +1,449 @@
+// fp4_quant.cu -- microscaled 4-bit floating point (e2m1): quantization of
+// bf16 rows and fp32 weights, dequantization, and the tiling of block scales.
+//
+// Formats (OCP Microscaling Formats v1.0 for "mx"; the two-level block-16
+// e4m3 form for "nv"):
+//   MX  blocks of 32 features, ue8m0 scale byte E = floor(log2 a) - 2 + 127
+//       (a the block's largest magnitude, E clamped to 0..254), code =
+//       e2m1(x / 2^(E - 127)), nearest, ties to even, saturating at 6.
+//   NV  per row s = the least power of two with max|row| <= 2688 s (2688 =
+//       6 * 448), at least 2^-110; blocks of 16 features, ue4m3 scale d =
+//       e4m3(fp32(a / s / 6)), code = e2m1(x / (d s)) (0 where d = 0).
+// The row scale is a power of two so that x / s is exact and a code depends
+// on the exact quotient alone: a general fp32 scale would gain nothing (the
+// e4m3 block scale absorbs any factor below 2) and would round x / (d s)
+// twice.  A block (MX) or row (NV) that holds a NaN or an infinity gets the
+// scale NaN (E = 255; s = NaN with block scales and codes 0), so everything
+// computed from it is NaN.
+//
+// Both are bound by HBM: one pass over x, 0.53 or 0.56 bytes written for 2
+// read.  A row stays in registers between the row maximum and the codes.
+#include <cuda_bf16.h>
+
+#include "fp4.h"
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace dq {
+namespace {
+
+// Eight fp32 values -> eight e2m1 codes (value 2i in the low nibble of byte
+// i), nearest with ties to even, saturating; -0 keeps its sign.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_byte(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+  return r & 0xffu;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(byte)));
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h2));
+  return f;
+}
+
+// 2^e for -149 <= e <= 127, from its bits.
+__device__ __forceinline__ float pow2i(int e) {
+  return e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23)
+                   : __uint_as_float(1u << (e + 149));
+}
+
+// Scale byte and the factor that takes x to its code's range, for a block of
+// largest magnitude `a` (fp32 bits, any payload for NaN).
+__device__ __forceinline__ uint32_t mx_scale(uint32_t abits, float& inv) {
+  if (abits >= 0x7f800000u) {
+    inv = 0.0f;
+    return 255u;
+  }
+  // floor(log2 a): subnormals (and 0) lie below every clamped scale
+  const int e = max(static_cast<int>(abits >> 23) - 2, 0);
+  inv = pow2i(127 - e);
+  return static_cast<uint32_t>(e);
+}
+
+// log2 of the NV row scale for the row's largest magnitude (fp32 bits, finite).
+__device__ __forceinline__ int nv_row_exp(uint32_t abits) {
+  // a = 1.f * 2^e <= 2688 * 2^p, 2688 = 1.3125 * 2^11
+  const int e = static_cast<int>(abits >> 23) - 127;
+  const int p = e - ((abits & 0x7fffffu) <= 0x280000u ? 11 : 10);
+  return max(p, -110);
+}
+
+// Code of one value against the scale d s of its block, |x| / s = ax exact:
+// the number of rounding borders (ties to the even code) that ax passes.
+// border * d has at most 7 significant bits, so every comparison is exact.
+__device__ __forceinline__ uint32_t e2m1_by_borders(float ax, float d, bool neg) {
+  uint32_t c = ax > 0.25f * d;
+  c += ax >= 0.75f * d;
+  c += ax > 1.25f * d;
+  c += ax >= 1.75f * d;
+  c += ax > 2.5f * d;
+  c += ax >= 3.5f * d;
+  c += ax > 5.0f * d;
+  c = d > 0.0f ? c : 0u;
+  return c | (neg ? 8u : 0u);
+}
+
+// ---------------------------------------------------------------- bf16 rows
+// Register-resident: 2^tpr_log2 (32..256) threads own a row, up to VPT
+// 16-byte vectors (8 features) each.  An NV block is 2 lanes, an MX block 4.
+// For NV codes the quotient is x * c with c = 1 / (s d) rounded: within 2^-23
+// of x / (s d).  X = x / s has 8 significant bits and border * d at most 7, so
+// the exact quotient either equals a border or is at least 2^-10 away from it
+// (2^-8 relative, the least border being 1/4); rounding the product to a
+// multiple of 2^-10 (one addition and subtraction of 1.5 * 2^13) therefore
+// restores ties exactly and moves nothing across a border.
+template <bool NV, int VPT>
+__global__ void __launch_bounds__(256) fp4_rows_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+                                                       int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
+                                                       uint8_t* __restrict__ sf, int64_t sf_atoms,
+                                                       float* __restrict__ s_row, int tpr_log2) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tpr = 1 << tpr_log2;
+  const int t = threadIdx.x & (tpr - 1);
+  const int r_local = threadIdx.x >> tpr_log2;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 >> tpr_log2) + r_local;
+  const int nv = static_cast<int>(K / 8);
+  const bool in = row < M;               // rows up to the next multiple of 128 get zero scales
+  __shared__ uint32_t warp_max[8];
+
+  uint4 v[VPT];
+  const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int vi = t + i * tpr;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (in && vi < nv) v[i] = __ldcs(xr + vi);
+  }
+  // magnitudes order like their bits, NaN above infinity above the rest
+  uint32_t top[VPT];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const uint32_t m = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+    uint32_t b = max(m & 0xffffu, m >> 16);
+    b = max(b, __shfl_xor_sync(0xffffffffu, b, 1));
+    if (!NV) b = max(b, __shfl_xor_sync(0xffffffffu, b, 2));
+    top[i] = b << 16;                    // fp32 bits
+    amax = max(amax, top[i]);
+  }
+  float inv_s = 1.0f;
+  bool bad_row = false;
+  if constexpr (NV) {
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (tpr > 32) {
+      const int warp = threadIdx.x >> 5;
+      if ((threadIdx.x & 31) == 0) warp_max[warp] = amax;
+      __syncthreads();
+      const int wpr = tpr >> 5;
+      amax = 0;
+      for (int w = 0; w < wpr; ++w) amax = max(amax, warp_max[r_local * wpr + w]);
+    }
+    bad_row = amax >= 0x7f800000u;
+    const int p = nv_row_exp(amax);
+    inv_s = pow2i(-p);
+    if (t == 0 && in) s_row[row] = bad_row ? __uint_as_float(0x7fc00000u) : pow2i(p);
+  }
+  const int64_t srow_off = (row >> 7) * sf_atoms * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+  uint8_t* qr = q + row * ldq;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int vi = t + i * tpr;
+    uint32_t byte;
+    float c;
+    bool zero;
+    if constexpr (NV) {
+      byte = e4m3_byte(__fdiv_rn(__uint_as_float(top[i]) * inv_s, 6.0f));
+      if (bad_row) byte = 0;
+      zero = byte == 0;
+      c = zero ? 0.0f : __fdiv_rn(1.0f, e4m3_value(byte)) * inv_s;
+    } else {
+      byte = mx_scale(top[i], c);
+      zero = byte == 255u;
+    }
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    float y[8];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      y[2 * h] = __uint_as_float(w[h] << 16) * c;
+      y[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u) * c;
+      if constexpr (NV) {
+        y[2 * h] = __fsub_rn(__fadd_rn(y[2 * h], 12288.0f), 12288.0f);
+        y[2 * h + 1] = __fsub_rn(__fadd_rn(y[2 * h + 1], 12288.0f), 12288.0f);
+      }
+    }
+    const uint32_t codes = zero ? 0u : e2m1x8(y);
+    // four neighbouring blocks' scale bytes as one word
+    uint32_t word = vi < nv ? byte << (8 * ((vi >> (NV ? 1 : 2)) & 3)) : 0u;
+    word |= __shfl_xor_sync(0xffffffffu, word, NV ? 2 : 4);
+    word |= __shfl_xor_sync(0xffffffffu, word, NV ? 4 : 8);
+    if (vi < nv) {
+      if (in) *reinterpret_cast<uint32_t*>(qr + static_cast<int64_t>(vi) * 4) = codes;
+      if ((vi & (NV ? 7 : 15)) == 0)
+        *reinterpret_cast<uint32_t*>(sf + srow_off + static_cast<int64_t>(vi >> (NV ? 3 : 4)) * 512) = in ? word : 0u;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ float elem_f32(const T* p);
+template <>
+__device__ __forceinline__ float elem_f32<uint16_t>(const uint16_t* p) {
+  return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+}
+template <>
+__device__ __forceinline__ float elem_f32<float>(const float* p) {
+  return *p;
+}
+
+// Any stride, alignment or row length, and fp32 weights: one CTA per row, two
+// passes over the row (the second from L2).  A thread takes one group of four
+// blocks at a time, so a scale word has one writer.
+template <typename T, bool NV>
+__global__ void __launch_bounds__(256) fp4_generic_kernel(const T* __restrict__ x, int64_t M, int64_t rows,
+                                                          int64_t K, int64_t ldx, uint8_t* __restrict__ q,
+                                                          int64_t ldq, uint8_t* __restrict__ sf, int64_t sf_atoms,
+                                                          float* __restrict__ s_row) {
+  constexpr int B = NV ? 16 : 32;
+  __shared__ uint32_t warp_max[8];
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const bool in = row < M;
+    const T* xr = x + row * ldx;
+    uint32_t amax = 0;
+    if (NV) {
+      if (in)
+        for (int64_t k = threadIdx.x; k < K; k += 256) amax = max(amax, __float_as_uint(elem_f32(xr + k)) & 0x7fffffffu);
+      amax = __reduce_max_sync(0xffffffffu, amax);
+      __syncthreads();                   // the previous row's maxima have been read
+      if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
+      __syncthreads();
+      for (int w = 0; w < 8; ++w) amax = max(amax, warp_max[w]);
+    }
+    const bool bad_row = amax >= 0x7f800000u;
+    const int p = nv_row_exp(amax);
+    const float inv_s = NV ? pow2i(-p) : 1.0f;
+    if (NV && threadIdx.x == 0 && in) s_row[row] = bad_row ? __uint_as_float(0x7fc00000u) : pow2i(p);
+    uint8_t* qr = q + row * ldq;
+    for (int64_t g = threadIdx.x; g < sf_atoms; g += 256) {
+      uint32_t word = 0;
+      for (int b = 0; in && b < 4; ++b) {
+        const int64_t k0 = (g * 4 + b) * B;
+        if (k0 >= K) break;
+        uint32_t top = 0;
+        for (int j = 0; j < B; ++j) top = max(top, __float_as_uint(elem_f32(xr + k0 + j)) & 0x7fffffffu);
+        uint32_t byte;
+        float c = 0.0f, d = 0.0f;
+        if (NV) {
+          byte = bad_row ? 0u : e4m3_byte(__fdiv_rn(__uint_as_float(top) * inv_s, 6.0f));
+          d = e4m3_value(byte);
+        } else {
+          byte = mx_scale(top, c);
+        }
+        word |= byte << (8 * b);
+        for (int j = 0; j < B; j += 8) {
+          uint32_t codes = 0;
+          if (NV) {
+            for (int u = 0; u < 8; ++u) {
+              const float f = elem_f32(xr + k0 + j + u);
+              codes |= e2m1_by_borders(fabsf(f) * inv_s, d, __float_as_uint(f) >> 31) << (4 * u);
+            }
+            if (bad_row) codes = 0;
+          } else if (byte != 255u) {
+            float y[8];
+            for (int u = 0; u < 8; ++u) y[u] = elem_f32(xr + k0 + j + u) * c;
+            codes = e2m1x8(y);
+          }
+          uint8_t* o = qr + (k0 + j) / 2;
+          for (int u = 0; u < 4; ++u) o[u] = static_cast<uint8_t>(codes >> (8 * u));
+        }
+      }
+      *reinterpret_cast<uint32_t*>(sf + ((row >> 7) * sf_atoms + g) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4) =
+          word;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- dequantize
+// One thread per 16 codes: w = bf16((e2m1 * d) * s), the block product exact.
+template <bool NV>
+__global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
+                                                          const float* __restrict__ s_row, int64_t M, int64_t K,
+                                                          int64_t sf_atoms, uint16_t* __restrict__ out) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t per_row = K / 16;
+  const int64_t n = M * per_row;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = i / per_row, u = i - row * per_row;
+    const uint2 c = *reinterpret_cast<const uint2*>(q + i * 8);
+    const int64_t blk = NV ? u : u >> 1;
+    const uint32_t byte =
+        __ldg(sf + ((row >> 7) * sf_atoms + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3));
+    float d;
+    if (NV) d = e4m3_value(byte);
+    else d = byte == 255u ? __uint_as_float(0x7fc00000u) : pow2i(static_cast<int>(byte) - 127);
+    const float s = s_row != nullptr ? __ldg(s_row + row) : 1.0f;
+    uint32_t o[8];
+#pragma unroll
+    for (int h = 0; h < 8; ++h) {
+      const uint32_t b = ((h < 4 ? c.x : c.y) >> (8 * (h & 3))) & 0xffu;
+      uint32_t h2;
+      asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h2) : "r"(b));
+      float lo, hi;
+      asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+          : "=f"(lo), "=f"(hi)
+          : "r"(h2));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[h]) : "f"(__fmul_rn(__fmul_rn(hi, d), s)), "f"(__fmul_rn(__fmul_rn(lo, d), s)));
+    }
+    uint4* dst = reinterpret_cast<uint4*>(out + i * 16);
+    __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+  }
+}
+
+// Block scales [rows, blocks] -> tiles of 128 rows x 4 blocks, zero padded.
+__global__ void __launch_bounds__(256) fp4_tile_kernel(const uint8_t* __restrict__ src, int64_t rows, int64_t blocks,
+                                                       int64_t atoms, int64_t total, uint8_t* __restrict__ dst) {
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t tile = i >> 9;
+    const int in = static_cast<int>(i & 511);
+    const int64_t r = (tile / atoms) * 128 + (in >> 4) + ((in >> 2) & 3) * 32;
+    const int64_t b = (tile % atoms) * 4 + (in & 3);
+    dst[i] = r < rows && b < blocks ? src[r * blocks + b] : 0;
+  }
+}
+
+// Programmatic (early) launch: every kernel here executes griddep_wait()
+// before its first global access.
+template <typename... P, typename... A>
+dq_status launch(void (*kernel)(P...), int64_t blocks, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  return e == cudaSuccess ? DQ_OK : cuda_fail(e);
+}
+
+constexpr int64_t kMaxGrid = 1 << 20;
+
+template <typename T, bool NV>
+dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* sf, float* s_row,
+                   cudaStream_t stream) {
+  const int64_t rows = (M + 127) / 128 * 128;
+  const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
+  if constexpr (sizeof(T) == 2) {
+    if (K <= 16384 && ldx % 8 == 0 && aligned(x, 16) && ldq % 4 == 0 && aligned(q, 4)) {
+      // 4 vectors per thread where 256 threads hold the row so, else 8
+      const int64_t nv = K / 8;
+      int vpt = nv <= 32 ? 1 : nv <= 64 ? 2 : 4;
+      int lg = 5;
+      while (lg < 8 && (static_cast<int64_t>(vpt) << lg) < nv) ++lg;
+      if ((static_cast<int64_t>(vpt) << lg) < nv) vpt = 8;
+      const int64_t blocks = (rows + (256 >> lg) - 1) / (256 >> lg);
+      if (blocks > 0x7fffffff) return DQ_ERR_UNSUPPORTED;
+      auto k = vpt == 1 ? fp4_rows_kernel<NV, 1> : vpt == 2 ? fp4_rows_kernel<NV, 2>
+               : vpt == 4 ? fp4_rows_kernel<NV, 4> : fp4_rows_kernel<NV, 8>;
+      return launch(k, blocks, stream, x, M, K, ldx, q, ldq, sf, atoms, s_row, lg);
+    }
+  }
+  return launch(fp4_generic_kernel<T, NV>, rows < kMaxGrid ? rows : kMaxGrid, stream, x, M, rows, K, ldx, q, ldq, sf,
+                atoms, s_row);
+}
+
+template <typename T>
+dq_status quantize_entry(const T* x, int64_t M, int64_t K, int64_t ldx, int fmt, uint8_t* q, int64_t ldq, uint8_t* sf,
+                         float* s, dq_stream_t stream) {
+  const bool nv = fmt == DQ_FP4_NV;
+  if ((!nv && fmt != DQ_FP4_MX) || M < 0 || K < 1 || ldx < K || ldq < K / 2) return DQ_ERR_INVALID_ARG;
+  if (M > 0 && (x == nullptr || q == nullptr || sf == nullptr || (nv && s == nullptr))) return DQ_ERR_INVALID_ARG;
+  if (K % 32 != 0 || M > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (!aligned(sf, 16) || !aligned(s, 4) || !aligned(x, sizeof(T))) return DQ_ERR_UNSUPPORTED;
+  DeviceInfo* d = nullptr;
+  const dq_status st = current_device(&d);
+  if (st != DQ_OK) return st;
+  if (M == 0) return DQ_OK;
+  auto cs = reinterpret_cast<cudaStream_t>(stream);
+  return nv ? quantize<T, true>(x, M, K, ldx, q, ldq, sf, s, cs) : quantize<T, false>(x, M, K, ldx, q, ldq, sf, s, cs);
+}
+
+}  // namespace
+}  // namespace dq
+
+using namespace dq;
+
+extern "C" {
+
+size_t dq_fp4_scales_size(int64_t rows, int64_t K, int fmt) {
+  if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || rows < 0 || K < 1 || K % 32 != 0 || rows > kFp4MaxDim || K > kFp4MaxDim)
+    return 0;
+  return static_cast<size_t>((rows + 127) / 128 * fp4_atoms(K, fmt) * 512);
+}
+
+dq_status dq_quantize_rows_fp4(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, int fmt, uint8_t* q, int64_t ldq,
+                               uint8_t* sf, float* s_row, dq_stream_t stream) {
+  return quantize_entry(static_cast<const uint16_t*>(x_bf16), M, K, ldx, fmt, q, ldq, sf, s_row, stream);
+}
+
+dq_status dq_quantize_weight_fp4(const float* w, int64_t N, int64_t K, int64_t ldw, int fmt, uint8_t* wq, int64_t ldwq,
+                                 uint8_t* sf, float* s_col, dq_stream_t stream) {
+  return quantize_entry(w, N, K, ldw, fmt, wq, ldwq, sf, s_col, stream);
+}
+
+dq_status dq_fp4_dequantize(const uint8_t* q, const uint8_t* sf, const float* s, int64_t M, int64_t K, int fmt,
+                            void* out_bf16, dq_stream_t stream) {
+  if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || M < 0 || K < 1) return DQ_ERR_INVALID_ARG;
+  if (M > 0 && (q == nullptr || sf == nullptr || out_bf16 == nullptr)) return DQ_ERR_INVALID_ARG;
+  if (K % 32 != 0 || M > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(sf, 16) || !aligned(out_bf16, 16) || !aligned(s, 4)) return DQ_ERR_UNSUPPORTED;
+  DeviceInfo* d = nullptr;
+  const dq_status st = current_device(&d);
+  if (st != DQ_OK) return st;
+  if (M == 0) return DQ_OK;
+  const int64_t want = (M * (K / 16) + 255) / 256;
+  const int64_t blocks = want < kMaxGrid ? want : kMaxGrid;
+  auto cs = reinterpret_cast<cudaStream_t>(stream);
+  return launch(fmt == DQ_FP4_NV ? fp4_dequant_kernel<true> : fp4_dequant_kernel<false>, blocks, cs, q, sf, s, M, K,
+                fp4_atoms(K, fmt), static_cast<uint16_t*>(out_bf16));
+}
+
+dq_status dq_fp4_tile_scales(const uint8_t* scales, int64_t rows, int64_t K, int fmt, uint8_t* sf, dq_stream_t stream) {
+  if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || rows < 0 || K < 1) return DQ_ERR_INVALID_ARG;
+  if (rows > 0 && (scales == nullptr || sf == nullptr)) return DQ_ERR_INVALID_ARG;
+  if (K % 32 != 0 || rows > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (!aligned(sf, 16)) return DQ_ERR_UNSUPPORTED;
+  DeviceInfo* d = nullptr;
+  const dq_status st = current_device(&d);
+  if (st != DQ_OK) return st;
+  if (rows == 0) return DQ_OK;
+  const int64_t total = static_cast<int64_t>(dq_fp4_scales_size(rows, K, fmt));
+  const int64_t want = (total + 255) / 256;
+  return launch(fp4_tile_kernel, want < kMaxGrid ? want : kMaxGrid, reinterpret_cast<cudaStream_t>(stream), scales, rows,
+                K / (fmt == DQ_FP4_NV ? 16 : 32), fp4_atoms(K, fmt), total, sf);
+}
+
+}  // extern "C"
