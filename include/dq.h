@@ -478,8 +478,16 @@ DQ_API dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float
  * dq_act8_pack: x bf16 [M, K] (row stride ldx, any 2-byte aligned address;
  *   8-byte aligned rows take wide loads) -> codes, scales.
  * dq_act8_unpack: codes, scales -> out bf16 [M, K] contiguous.
- * Requirements: K % 16 == 0, M >= 0, M, K <= 2^30; codes, scales and out
- * 16-byte aligned.
+ * dq_act8_weight_grad: the gradients of out = x W^T + bias from dY bf16 [M, N]
+ *   (row stride lddy) and the checkpoint of x:
+ *     dW[n, k] = sum_m dY[m, n] x8[m, k],   db[n] = sum_m dY[m, n].
+ *   dW [N, K] contiguous, bf16 (rounded once) or fp32; with `accumulate` (fp32
+ *   only) both gradients are added to what dw and db hold.  db fp32 [N] or
+ *   NULL.  Sums are fp32 on the bf16 tensor cores (tcgen05.mma kind::f16; both
+ *   factors are exact bf16 numbers); their order is the schedule's and does
+ *   not change from call to call.  M == 0 writes zeros (accumulate: nothing).
+ * Requirements: K % 16 == 0, N % 8 == 0, lddy % 8 == 0, M >= 0, M, N, K <=
+ * 2^30; pointers 16-byte aligned (x: above).
  * ------------------------------------------------------------------------ */
 DQ_API size_t dq_act8_codes_size(int64_t M, int64_t K);
 DQ_API size_t dq_act8_scales_size(int64_t M, int64_t K);
@@ -487,6 +495,9 @@ DQ_API dq_status dq_act8_pack(const void* x_bf16, int64_t M, int64_t K, int64_t 
                               dq_stream_t stream);
 DQ_API dq_status dq_act8_unpack(const int8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out_bf16,
                                 dq_stream_t stream);
+DQ_API dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t lddy, const int8_t* codes,
+                                     const uint8_t* scales, int64_t K, void* dw, dq_out_dtype dw_dtype, int accumulate,
+                                     float* db, dq_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Measurement knobs.  Process-wide settings read by every later launch from

@@ -73,6 +73,7 @@ _PROTOS = {
     "dq_act8_scales_size": (_SZ, [_I64, _I64]),
     "dq_act8_pack": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "dq_act8_unpack": (_I32, [_P, _P, _I64, _I64, _P, _P]),
+    "dq_act8_weight_grad": (_I32, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I32, _I32, _P, _P]),
 }
 
 
@@ -880,6 +881,49 @@ def dq_act8_unpack(codes, scales, M: int, out=None, stream=None) -> torch.Tensor
     _same_device(codes, scales=scales, out=out)
     _check(lib.dq_act8_unpack(_ptr(codes), _ptr(scales), M, K, _ptr(out), _stream(stream)), "dq_act8_unpack")
     return out
+
+
+def dq_act8_weight_grad(dy, codes, scales, out=None, out_dtype="bf16", accumulate: bool = False, bias_grad=False,
+                        stream=None):
+    """(dW, db) of a linear layer from dy bf16 [M, N] (row stride dy.stride(0))
+    and its input's 8-bit checkpoint: dW[n, k] = sum_m dy[m, n] x[m, k] as bf16
+    or fp32 [N, K], db[n] = sum_m dy[m, n] as fp32 [N].  `bias_grad`: False (db
+    is None), True, or the fp32 tensor to fill.  With accumulate=True (fp32
+    `out` given, and `bias_grad` a tensor or False) both are added to what the
+    tensors hold."""
+    if out_dtype in ("f32", "float32", torch.float32, DQ_OUT_F32):
+        oc, odt = DQ_OUT_F32, torch.float32
+    elif out_dtype in ("bf16", torch.bfloat16, DQ_OUT_BF16):
+        oc, odt = DQ_OUT_BF16, torch.bfloat16
+    else:
+        raise ValueError(f"out_dtype {out_dtype!r}")
+    _need(dy, torch.bfloat16, "dy", 2)
+    ld = _rows(dy, "dy")
+    M, N = dy.shape
+    K = _act8_operand(codes, scales, M)
+    if accumulate and (out is None or oc != DQ_OUT_F32 or bias_grad is True):
+        raise ValueError("accumulate needs the fp32 tensors to add to")
+    if out is None:
+        out = torch.empty((N, K), dtype=odt, device=dy.device)
+    _need(out, odt, "out", 2)
+    _contig(out, "out")
+    if tuple(out.shape) != (N, K):
+        raise ValueError(f"out must be {(N, K)}")
+    db = None
+    if bias_grad is True:
+        db = torch.empty((N,), dtype=torch.float32, device=dy.device)
+    elif bias_grad is not False and bias_grad is not None:
+        db = bias_grad
+        _need(db, torch.float32, "bias_grad", 1)
+        _contig(db, "bias_grad")
+        if db.numel() != N:
+            raise ValueError("bias_grad length mismatch")
+    _same_device(dy, codes=codes, scales=scales, out=out, bias_grad=db)
+    if M <= 1:                        # a single row has no stride to speak of
+        ld = (ld + 7) // 8 * 8
+    _check(lib.dq_act8_weight_grad(_ptr(dy), M, N, ld, _ptr(codes), _ptr(scales), K, _ptr(out), oc, int(accumulate),
+                                   _ptr(db), _stream(stream)), "dq_act8_weight_grad")
+    return out, db
 
 
 # ---------------------------------------------------------------- layer
