@@ -284,14 +284,29 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     const int q = warp & 3;                      // TMEM sub-partition
     const uint32_t feat = static_cast<uint32_t>(q * 32 + lane);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g.slot_col);
-    long long it = 0;                            // the CTA's step counter, over its units
+    int stage = 0, slot = 0, old = 0;            // ring positions of the CTA's current step, over its units
+    uint32_t phase = 0, old_phase = 0;
+    int warm = g.slots;                          // steps until a slot is used again
+    int turn = 0;
     bool ok = true;
+    auto advance = [&]() {
+      turn ^= 1;
+      if (++stage == g.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      if (++slot == g.slots) slot = 0;
+      if (warm > 0) {
+        --warm;
+      } else if (++old == g.stages) {
+        old = 0;
+        old_phase ^= 1;
+      }
+    };
     for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const GradUnit t = grad_unit(g, u);
-      for (int s = t.s0; s < t.s1; ++s, ++it) {
-        if ((it & 1) != grp) continue;
-        const int stage = static_cast<int>(it % g.stages);
-        const uint32_t phase = static_cast<uint32_t>((it / g.stages) & 1);
+      for (int s = t.s0; s < t.s1; ++s, advance()) {
+        if (turn != grp) continue;
         bool w = pipe::wait(smem_u32(full + stage), phase, g.wait, abort_flag);
         const uint32_t sq = base + static_cast<uint32_t>(stage) * stage_bytes + y_bytes;
         uint32_t r[32];
@@ -309,18 +324,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             }
           }
           // the slot's previous MMAs have completed
-          if (it >= g.slots) {
-            const long long j = it - g.slots;
-            w = pipe::wait(smem_u32(empty + static_cast<int>(j % g.stages)), static_cast<uint32_t>((j / g.stages) & 1),
-                           g.wait, abort_flag);
-          }
+          if (warm == 0) w = pipe::wait(smem_u32(empty + old), old_phase, g.wait, abort_flag);
         }
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        tmem_st_32x32b_x32(lane_base + static_cast<uint32_t>(it % g.slots) * WG_SLOT_COLS, r);
+        tmem_st_32x32b_x32(lane_base + static_cast<uint32_t>(slot) * WG_SLOT_COLS, r);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();

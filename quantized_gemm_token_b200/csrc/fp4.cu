@@ -81,8 +81,11 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, ui
 // prologue, pipeline ends and epilogue.  Few channel tiles: the features are
 // split over a cluster of up to 8 CTAs, whose fp32 partial tiles are added
 // through distributed shared memory in split order.
-//   warp 0 producer, warp 1 scale copies and MMAs, all six warps the epilogue.
-constexpr int FS_THREADS = 192;
+//   warps 0 and 6..8 producers (one of the stage's four copies each: a copy
+//   holds its thread for some hundred cycles, a stage must not take longer
+//   than its 20 KB at HBM rate), warp 1 scale copies and MMAs, warps 2..5
+//   drain the accumulator, all nine write the output.
+constexpr int FS_THREADS = 288;
 constexpr int FS_MAX_STAGES = 8;
 constexpr int FS_BAR_BYTES = 256;
 
@@ -162,20 +165,21 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
   const int kb0 = static_cast<int>(static_cast<int64_t>(split) * g.kb_total / g.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(split + 1) * g.kb_total / g.splits);
 
-  if (warp == 0) {
+  if (warp == 0 || warp >= 6) {
     if (lane == 0) {
+      const int prod = warp == 0 ? 0 : warp - 5;     // 0 weight, 1 its scales, 2 tokens, 3 their scales
+      const void* const map = prod == 0 ? &tm_w : prod == 1 ? &tm_sw : prod == 2 ? &tm_x : &tm_sx;
+      const uint32_t off = prod == 0 ? 0u : prod == 2 ? W_BYTES : W_BYTES + x_bytes + (prod == 3 ? S_BYTES : 0u);
+      const int dx = prod == 0 || prod == 2 ? F4_KB : T * 64;
+      const int y = prod == 0 ? nt * 128 : prod == 1 ? nt : prod == 2 ? tt * g.bn : tt * g.bn / 128;
       int stage = 0;
       uint32_t phase = 0;
       int issued = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!pipe::wait(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) break;
         const uint32_t fb = smem_u32(full + stage);
-        const uint32_t sw = base + static_cast<uint32_t>(stage) * stage_bytes;
-        mbar_arrive_expect_tx(fb, stage_bytes);
-        tma_load_2d(sw, &tm_w, fb, kb * F4_KB, nt * 128);
-        tma_load_2d(sw + W_BYTES + x_bytes, &tm_sw, fb, kb * T * 64, nt);
-        tma_load_2d(sw + W_BYTES, &tm_x, fb, kb * F4_KB, tt * g.bn);
-        tma_load_2d(sw + W_BYTES + x_bytes + S_BYTES, &tm_sx, fb, kb * T * 64, tt * g.bn / 128);
+        if (prod == 0) mbar_arrive_expect_tx(fb, stage_bytes);
+        tma_load_2d(base + static_cast<uint32_t>(stage) * stage_bytes + off, map, fb, kb * dx, y);
         ++issued;
         if (++stage == g.stages) {
           stage = 0;
@@ -189,20 +193,21 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      const uint32_t col_x = static_cast<uint32_t>(((tt * g.bn) % 128) / 32);   // first token's scale column
+      int stage = 0, slot = 0, old = 0;
+      uint32_t phase = 0, old_phase = 0;
       for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
         if (!pipe::wait(smem_u32(full + stage), phase, g.wait, abort_flag)) break;
-        // the scale slot's previous user must have completed
-        if (i >= g.sf_slots) {
-          const int j = i - g.sf_slots;
-          if (!pipe::wait(smem_u32(empty + j % g.stages), static_cast<uint32_t>((j / g.stages) & 1), g.wait, abort_flag))
-            break;
+        if (i >= g.sf_slots) {             // the scale slot's previous user has completed
+          if (!pipe::wait(smem_u32(empty + old), old_phase, g.wait, abort_flag)) break;
+          if (++old == g.stages) {
+            old = 0;
+            old_phase ^= 1;
+          }
         }
         tc_fence_after();
         const uint32_t sw = base + static_cast<uint32_t>(stage) * stage_bytes;
-        const uint32_t sfa = tmem + static_cast<uint32_t>(g.sf_col + (i % g.sf_slots) * SF_COLS);
+        const uint32_t sfa = tmem + static_cast<uint32_t>(g.sf_col + slot * SF_COLS);
+        if (++slot == g.sf_slots) slot = 0;
         const uint32_t sfb = sfa + T * 4;
         const int steps = min(4, g.ks_total - 4 * kb);
         const uint64_t da = sf_desc(sw + W_BYTES + x_bytes), db = sf_desc(sw + W_BYTES + x_bytes + S_BYTES);
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
           if (k < steps) {
             const int t = NV ? k : k >> 1;
             mma_fp4<1, NV>(tmem, ad + 2 * k, bd + 2 * k, idesc_fp4(128, g.bn, NV, NV ? 0 : k & 1), sfa + 4 * t,
-                           sfb + 4 * t + col_x, (i > 0 || k > 0) ? 1u : 0u);
+                           sfb + 4 * t, (i > 0 || k > 0) ? 1u : 0u);
           }
         mma_commit(smem_u32(empty + stage));
         if (++stage == g.stages) {
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
   // consumed stage ring), from where the split's CTAs add their shares.
   const bool ok = pipe::wait(smem_u32(accf), 0, g.wait, abort_flag);
   tc_fence_after();
-  if (warp >= 2 && __all_sync(0xffffffffu, ok)) {
+  if (warp >= 2 && warp < 6 && __all_sync(0xffffffffu, ok)) {
     const int q = warp & 3;
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     for (int c0 = 0; c0 < g.bn; c0 += 16) {
@@ -307,8 +312,9 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
 // its own rows' scale tiles and ALL of the tile's weight scale tiles (each
 // SM's tensor core multiplies its rows with every column, so both tensor
 // memories need every column's scales).
-//   warp 0 producer, warp 1 (leader) scale copies and MMAs, warps 2..9
-//   epilogue, two per TMEM sub-partition on alternate 32-column chunks.
+//   warps 0 and 10..12 producers (one copy per stage each), warp 1 (leader)
+//   scale copies and MMAs, warps 2..9 epilogue, two per TMEM sub-partition on
+//   alternate 32-column chunks.
 template <int BN, bool NV>
 struct CfgP {
   static constexpr int T = f4_tiles(NV);
@@ -330,7 +336,7 @@ struct CfgP {
   static constexpr int SF_COL0 = ACC_BUFS * BN;
   static constexpr int SLOTS_FIT = (512 - SF_COL0) / SF_COLS;
   static constexpr int SLOTS = SLOTS_FIT < STAGES ? SLOTS_FIT : STAGES;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS + 96;   // three more producer warps
   static constexpr int OFF_SA = STAGES * (A_BYTES + B_BYTES);
   static constexpr int OFF_SB = OFF_SA + STAGES * SA_BYTES;
   static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;
@@ -408,28 +414,35 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
   griddep_launch_dependents();
   griddep_wait();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer (both CTAs)
+  const int prod = warp == 0 ? 0 : warp - (1 + C::EPI_WARPS);   // 0, or 1..3 for the last three warps
+  if (warp == 0 || warp >= 2 + C::EPI_WARPS) {
+    // ------------------------------------------------------------ producers (both CTAs)
+    // A tensor copy holds its issuing thread for some hundred cycles, a stage's
+    // MMAs take 384 - 512: each of the four copies has a thread of its own.
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
+      const void* const map = prod == 0 ? &tm_a : prod == 1 ? &tm_b : prod == 2 ? &tm_sa : &tm_sb;
+      const uint32_t dst0 = prod == 0 ? sA : prod == 1 ? sB : prod == 2 ? sSA : sSB;
+      const uint32_t step = prod == 0 ? C::A_BYTES : prod == 1 ? C::B_BYTES : prod == 2 ? C::SA_BYTES : C::SB_BYTES;
+      const int dx = prod < 2 ? F4_KB : C::T * 64;
       for (int t = pair; ok && t < g.num_tiles; t += G) {
         const int ta = t / g.b_tiles;
         const int n0 = (t - ta * g.b_tiles) * BN;
+        const int y = prod == 0   ? ta * 256 + static_cast<int>(rank) * 128
+                      : prod == 1 ? n0 + static_cast<int>(rank) * (BN / 2)
+                      : prod == 2 ? ta * 2 + static_cast<int>(rank)
+                                  : n0 / 128;
         for (int kb = 0; kb < g.kb_total; ++kb) {
           if (!mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, g.wait, abort_flag)) {
             ok = false;
             break;
           }
           const uint32_t fb = smem_u32(full_bar + stage);
-          if (leader) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
-          const uint32_t fbl = map_to_rank(fb, 0);
-          tma_load_2d_pair(sA + stage * C::A_BYTES, &tm_a, fbl, kb * F4_KB, ta * 256 + static_cast<int>(rank) * 128);
-          tma_load_2d_pair(sB + stage * C::B_BYTES, &tm_b, fbl, kb * F4_KB, n0 + static_cast<int>(rank) * (BN / 2));
-          tma_load_2d_pair(sSA + stage * C::SA_BYTES, &tm_sa, fbl, kb * C::T * 64, ta * 2 + static_cast<int>(rank));
-          tma_load_2d_pair(sSB + stage * C::SB_BYTES, &tm_sb, fbl, kb * C::T * 64, n0 / 128);
+          if (leader && prod == 0) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
+          tma_load_2d_pair(dst0 + static_cast<uint32_t>(stage) * step, map, map_to_rank(fb, 0), kb * dx, y);
           ++issued;
           if (++stage == C::STAGES) {
             stage = 0;
@@ -462,7 +475,10 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
     if (leader && lane == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      long long it = 0;
+      int slot = 0;                       // scale slot of this stage
+      int warm = C::SLOTS;                // stages until a slot is used again
+      int old = 0;                        // stage (and its lap's parity) that used the slot before
+      uint32_t old_phase = 0;
       bool ok = true;
       const int ks_total = (g.K + 63) / 64;
       for (int t = pair; ok && t < g.num_tiles; t += G) {
@@ -471,21 +487,28 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
         if (!mbar_wait(smem_u32(acce_bar + acc), acc_phase ^ 1, g.wait, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
-        for (int kb = 0; kb < g.kb_total; ++kb, ++it) {
+        for (int kb = 0; kb < g.kb_total; ++kb) {
           if (!mbar_wait(smem_u32(full_bar + stage), phase, g.wait, abort_flag)) {
             ok = false;
             break;
           }
-          if (C::SLOTS < C::STAGES && it >= C::SLOTS) {   // the scale slot's previous user has completed
-            const long long j = it - C::SLOTS;
-            if (!mbar_wait(smem_u32(empty_bar + j % C::STAGES), static_cast<uint32_t>((j / C::STAGES) & 1), g.wait,
-                           abort_flag)) {
-              ok = false;
-              break;
+          if (C::SLOTS < C::STAGES) {
+            if (warm > 0) {
+              --warm;
+            } else {                      // the scale slot's previous user has completed
+              if (!mbar_wait(smem_u32(empty_bar + old), old_phase, g.wait, abort_flag)) {
+                ok = false;
+                break;
+              }
+              if (++old == C::STAGES) {
+                old = 0;
+                old_phase ^= 1;
+              }
             }
           }
           tc_fence_after();
-          const uint32_t sfa = tmem_base + C::SF_COL0 + static_cast<uint32_t>(it % C::SLOTS) * C::SF_COLS;
+          const uint32_t sfa = tmem_base + C::SF_COL0 + static_cast<uint32_t>(slot) * C::SF_COLS;
+          if (++slot == C::SLOTS) slot = 0;
           const uint32_t sfb = sfa + C::SF_A;
           const uint64_t da = sf_desc(sSA + stage * C::SA_BYTES), db = sf_desc(sSB + stage * C::SB_BYTES);
 #pragma unroll
@@ -624,12 +647,13 @@ dq_status launch_few(const uint8_t* A, const uint8_t* sfa, int64_t M, int64_t K,
   g.nt = static_cast<int>((N + 127) / 128);
   g.kb_total = static_cast<int>((K + F4_KE - 1) / F4_KE);
   g.ks_total = static_cast<int>((K + 63) / 64);
-  // As many CTAs per SM as three (two from 64 tokens): the smallest split that
-  // gives every slot a unit, as long as a unit keeps two stages of features.
-  const int per_sm = g.bn <= 48 ? 3 : 2;
+  // Two CTAs per SM.  All units resident at once share the memory's bandwidth
+  // evenly and end together, whatever their number per SM, so only too few of
+  // them call for a split.
+  const int per_sm = 2;
   const int64_t tiles = static_cast<int64_t>(g.nt) * g.tt;
   g.splits = 1;
-  while (g.splits < 8 && tiles * g.splits < static_cast<int64_t>(per_sm) * sm_count && g.kb_total / (2 * g.splits) >= 2)
+  while (g.splits < 8 && tiles * g.splits * 2 <= static_cast<int64_t>(per_sm) * sm_count && g.kb_total / (2 * g.splits) >= 2)
     g.splits *= 2;
   const int stage_bytes = 128 * F4_KB + g.bn * F4_KB + 2 * T * 512;
   const int limit = (227 * 1024 - per_sm * 1024) / per_sm;
