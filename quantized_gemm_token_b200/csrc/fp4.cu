@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
-    if (leader && lane == 0) {
+    if (leader) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       int slot = 0;                       // scale slot of this stage
@@ -484,11 +484,11 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
       for (int t = pair; ok && t < g.num_tiles; t += G) {
         // an odd tile of width 192 (or 64) starts in the middle of a scale row block
         const uint32_t col_b = static_cast<uint32_t>((((t % g.b_tiles) * BN) % 128) / 32);
-        if (!mbar_wait(smem_u32(acce_bar + acc), acc_phase ^ 1, g.wait, abort_flag)) break;
+        if (!mbar_wait_warp(smem_u32(acce_bar + acc), acc_phase ^ 1, g.wait, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kb = 0; kb < g.kb_total; ++kb) {
-          if (!mbar_wait(smem_u32(full_bar + stage), phase, g.wait, abort_flag)) {
+          if (!mbar_wait_warp(smem_u32(full_bar + stage), phase, g.wait, abort_flag)) {
             ok = false;
             break;
           }
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
             if (warm > 0) {
               --warm;
             } else {                      // the scale slot's previous user has completed
-              if (!mbar_wait(smem_u32(empty_bar + old), old_phase, g.wait, abort_flag)) {
+              if (!mbar_wait_warp(smem_u32(empty_bar + old), old_phase, g.wait, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -511,38 +511,44 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
           if (++slot == C::SLOTS) slot = 0;
           const uint32_t sfb = sfa + C::SF_A;
           const uint64_t da = sf_desc(sSA + stage * C::SA_BYTES), db = sf_desc(sSB + stage * C::SB_BYTES);
-#pragma unroll
-          for (int s = 0; s < C::T; ++s) {
-            cp_sf<2>(sfa + 4 * s, da + 32 * s);
-#pragma unroll
-            for (int r = 0; r < C::RB; ++r) cp_sf<2>(sfb + 4 * (s * C::RB + r), db + 32 * (r * C::T + s));
-          }
           const uint64_t ad = smem_desc_kmajor<128>(sA + stage * C::A_BYTES);
           const uint64_t bd = smem_desc_kmajor<128>(sB + stage * C::B_BYTES);
           const int steps = min(4, ks_total - 4 * kb);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps) {
-              const int s = NV ? k : k >> 1;
-              mma_fp4<2, NV>(d, ad + 2 * k, bd + 2 * k, idesc_fp4(256, BN, NV, NV ? 0 : k & 1), sfa + 4 * s,
-                             sfb + 4 * C::RB * s + col_b, (kb > 0 || k > 0) ? 1u : 0u);
+            for (int s = 0; s < C::T; ++s) {
+              cp_sf<2>(sfa + 4 * s, da + 32 * s);
+#pragma unroll
+              for (int r = 0; r < C::RB; ++r) cp_sf<2>(sfb + 4 * (s * C::RB + r), db + 32 * (r * C::T + s));
             }
-          mma_commit_pair_both(smem_u32(empty_bar + stage));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < steps) {
+                const int s = NV ? k : k >> 1;
+                mma_fp4<2, NV>(d, ad + 2 * k, bd + 2 * k, idesc_fp4(256, BN, NV, NV ? 0 : k & 1), sfa + 4 * s,
+                               sfb + 4 * C::RB * s + col_b, (kb > 0 || k > 0) ? 1u : 0u);
+              }
+            mma_commit_pair_both(smem_u32(empty_bar + stage));
+          }
+          __syncwarp();
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit_pair_both(smem_u32(accf_bar + acc));
+        if (elect_one()) mma_commit_pair_both(smem_u32(accf_bar + acc));
+        __syncwarp();
         if (++acc == C::ACC_BUFS) {
           acc = 0;
           acc_phase ^= 1;
         }
       }
-      mma_commit_pair(map_to_rank(smem_u32(drain_bar), 0));
+      if (elect_one()) mma_commit_pair(map_to_rank(smem_u32(drain_bar), 0));
+      __syncwarp();
       volatile int never = 0;
       mbar_wait(smem_u32(drain_bar), 0, g.wait, &never);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
