@@ -197,24 +197,24 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      const int chunks = g.bn / 64;
-      for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
-        const GradUnit t = grad_unit(g, u);
-        const int c0 = t.nt * chunks;
-        // the 3-D map covers whole chunks only: a tile that holds the ragged last one is loaded chunk by chunk
-        const bool whole = c0 + chunks <= g.full_chunks || g.N % 64 == 0;
-        for (int s = t.s0; s < t.s1; ++s) {
-          if (!pipe::wait(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(full + stage);
-          const uint32_t sy = base + static_cast<uint32_t>(stage) * stage_bytes;
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    const int chunks = g.bn / 64;
+    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      const GradUnit t = grad_unit(g, u);
+      const int c0 = t.nt * chunks;
+      // the 3-D map covers whole chunks only: a tile that holds the ragged last one is loaded chunk by chunk
+      const bool whole = c0 + chunks <= g.full_chunks || g.N % 64 == 0;
+      for (int s = t.s0; s < t.s1; ++s) {
+        if (!mbar_wait_warp(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = smem_u32(full + stage);
+        const uint32_t sy = base + static_cast<uint32_t>(stage) * stage_bytes;
+        if (elect_one()) {
           mbar_arrive_expect_tx(fb, y_bytes + WG_CODES + 256u);
           tma_load_2d(sy + y_bytes, &tm_q, fb, t.kt * 256, s * 4);
           tma_load_2d(sy + y_bytes + WG_CODES, &tm_e, fb, t.kt * 128, s * 2);
@@ -223,61 +223,65 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
           else
             for (int c = 0; c < chunks; ++c)
               tma_load_2d(sy + static_cast<uint32_t>(c) * 8192u, &tm_y2, fb, (c0 + c) * 64, s * WG_STEP);
-          ++issued;
-          if (++stage == g.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == g.stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      volatile int never = 0;
-      for (long long i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
-        pipe::wait(smem_u32(full + static_cast<int>(i % g.stages)), static_cast<uint32_t>((i / g.stages) & 1), g.wait,
-                   &never);
     }
+    volatile int never = 0;
+    for (long long i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
+      pipe::wait(smem_u32(full + static_cast<int>(i % g.stages)), static_cast<uint32_t>((i / g.stages) & 1), g.wait,
+                 &never);
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = idesc_grad(g.bn);
-      int stage = 0, acc = 0, slot = 0;
-      uint32_t phase = 0, aphase = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
-        const GradUnit t = grad_unit(g, u);
-        if (!pipe::wait(smem_u32(acce + acc), aphase ^ 1, g.wait, abort_flag)) break;
+    const uint32_t idesc = idesc_grad(g.bn);
+    int stage = 0, acc = 0, slot = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      const GradUnit t = grad_unit(g, u);
+      if (!mbar_wait_warp(smem_u32(acce + acc), aphase ^ 1, g.wait, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + static_cast<uint32_t>(acc * g.acc_cols);
+      for (int s = t.s0; s < t.s1; ++s) {
+        // the converters waited for the copies
+        if (!mbar_wait_warp(smem_u32(cvt + stage), phase, g.wait, abort_flag) ||
+            !mbar_wait_warp(smem_u32(full + stage), phase, g.wait, abort_flag)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * g.acc_cols);
-        for (int s = t.s0; s < t.s1; ++s) {
-          // the converters waited for the copies
-          if (!pipe::wait(smem_u32(cvt + stage), phase, g.wait, abort_flag) ||
-              !pipe::wait(smem_u32(full + stage), phase, g.wait, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t bd = smem_desc_mn(base + static_cast<uint32_t>(stage) * stage_bytes, 8192u);
-          const uint32_t a = tmem + static_cast<uint32_t>(g.slot_col + slot * WG_SLOT_COLS);
+        const uint64_t bd = smem_desc_mn(base + static_cast<uint32_t>(stage) * stage_bytes, 8192u);
+        const uint32_t a = tmem + static_cast<uint32_t>(g.slot_col + slot * WG_SLOT_COLS);
+        if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)      // 16 tokens: 8 columns of A, 2048 bytes of B
+          for (int j = 0; j < 4; ++j)        // 16 tokens: 8 columns of A, 2048 bytes of B
             mma_bf16_ts(d, a + 8 * j, bd + 128 * j, idesc, (s > t.s0 || j > 0) ? 1u : 0u);
           mma_commit(smem_u32(empty + stage));
-          if (++slot == g.slots) slot = 0;
-          if (++stage == g.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-        if (!ok) break;
-        mma_commit(smem_u32(accf + acc));
-        if (++acc == g.accs) {
-          acc = 0;
-          aphase ^= 1;
+        __syncwarp();
+        if (++slot == g.slots) slot = 0;
+        if (++stage == g.stages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      mma_commit(smem_u32(drain));
-      volatile int never = 0;
-      pipe::wait(smem_u32(drain), 0, g.wait, &never);
+      if (!ok) break;
+      if (elect_one()) mma_commit(smem_u32(accf + acc));
+      __syncwarp();
+      if (++acc == g.accs) {
+        acc = 0;
+        aphase ^= 1;
+      }
     }
+    if (elect_one()) mma_commit(smem_u32(drain));
+    __syncwarp();
+    volatile int never = 0;
+    pipe::wait(smem_u32(drain), 0, g.wait, &never);
   } else if (warp < WG_EPI_WARP0) {
     // ---------------------------------------------------------- converters
     const int grp = (warp - 2) >> 2;

@@ -81,11 +81,9 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, ui
 // prologue, pipeline ends and epilogue.  Few channel tiles: the features are
 // split over a cluster of up to 8 CTAs, whose fp32 partial tiles are added
 // through distributed shared memory in split order.
-//   warps 0 and 6..8 producers (one of the stage's four copies each: a copy
-//   holds its thread for some hundred cycles, a stage must not take longer
-//   than its 20 KB at HBM rate), warp 1 scale copies and MMAs, warps 2..5
-//   drain the accumulator, all nine write the output.
-constexpr int FS_THREADS = 288;
+//   warp 0 producer, warp 1 scale copies and MMAs, warps 2..5 drain the
+//   accumulator, all six write the output.
+constexpr int FS_THREADS = 192;
 constexpr int FS_MAX_STAGES = 8;
 constexpr int FS_BAR_BYTES = 256;
 
@@ -165,59 +163,59 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
   const int kb0 = static_cast<int>(static_cast<int64_t>(split) * g.kb_total / g.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(split + 1) * g.kb_total / g.splits);
 
-  if (warp == 0 || warp >= 6) {
-    if (lane == 0) {
-      const int prod = warp == 0 ? 0 : warp - 5;     // 0 weight, 1 its scales, 2 tokens, 3 their scales
-      const void* const map = prod == 0 ? &tm_w : prod == 1 ? &tm_sw : prod == 2 ? &tm_x : &tm_sx;
-      const uint32_t off = prod == 0 ? 0u : prod == 2 ? W_BYTES : W_BYTES + x_bytes + (prod == 3 ? S_BYTES : 0u);
-      const int dx = prod == 0 || prod == 2 ? F4_KB : T * 64;
-      const int y = prod == 0 ? nt * 128 : prod == 1 ? nt : prod == 2 ? tt * g.bn : tt * g.bn / 128;
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!pipe::wait(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) break;
-        const uint32_t fb = smem_u32(full + stage);
-        if (prod == 0) mbar_arrive_expect_tx(fb, stage_bytes);
-        tma_load_2d(base + static_cast<uint32_t>(stage) * stage_bytes + off, map, fb, kb * dx, y);
-        ++issued;
-        if (++stage == g.stages) {
-          stage = 0;
-          phase ^= 1;
+  if (warp == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_warp(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) break;
+      const uint32_t fb = smem_u32(full + stage);
+      const uint32_t sw = base + static_cast<uint32_t>(stage) * stage_bytes;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(fb, stage_bytes);
+        tma_load_2d(sw, &tm_w, fb, kb * F4_KB, nt * 128);
+        tma_load_2d(sw + W_BYTES + x_bytes, &tm_sw, fb, kb * T * 64, nt);
+        tma_load_2d(sw + W_BYTES, &tm_x, fb, kb * F4_KB, tt * g.bn);
+        tma_load_2d(sw + W_BYTES + x_bytes + S_BYTES, &tm_sx, fb, kb * T * 64, tt * g.bn / 128);
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == g.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    // every copy issued lands before the CTA can exit
+    volatile int never = 0;
+    for (int i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
+      pipe::wait(smem_u32(full + i % g.stages), static_cast<uint32_t>((i / g.stages) & 1), g.wait, &never);
+  } else if (warp == 1) {
+    int stage = 0, slot = 0, old = 0;
+    uint32_t phase = 0, old_phase = 0;
+    for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
+      if (!mbar_wait_warp(smem_u32(full + stage), phase, g.wait, abort_flag)) break;
+      if (i >= g.sf_slots) {               // the scale slot's previous user has completed
+        if (!mbar_wait_warp(smem_u32(empty + old), old_phase, g.wait, abort_flag)) break;
+        if (++old == g.stages) {
+          old = 0;
+          old_phase ^= 1;
         }
       }
-      // every copy issued lands before the CTA can exit
-      volatile int never = 0;
-      for (int i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
-        pipe::wait(smem_u32(full + i % g.stages), static_cast<uint32_t>((i / g.stages) & 1), g.wait, &never);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, slot = 0, old = 0;
-      uint32_t phase = 0, old_phase = 0;
-      for (int kb = kb0, i = 0; kb < kb1; ++kb, ++i) {
-        if (!pipe::wait(smem_u32(full + stage), phase, g.wait, abort_flag)) break;
-        if (i >= g.sf_slots) {             // the scale slot's previous user has completed
-          if (!pipe::wait(smem_u32(empty + old), old_phase, g.wait, abort_flag)) break;
-          if (++old == g.stages) {
-            old = 0;
-            old_phase ^= 1;
-          }
-        }
-        tc_fence_after();
-        const uint32_t sw = base + static_cast<uint32_t>(stage) * stage_bytes;
-        const uint32_t sfa = tmem + static_cast<uint32_t>(g.sf_col + slot * SF_COLS);
-        if (++slot == g.sf_slots) slot = 0;
-        const uint32_t sfb = sfa + T * 4;
-        const int steps = min(4, g.ks_total - 4 * kb);
-        const uint64_t da = sf_desc(sw + W_BYTES + x_bytes), db = sf_desc(sw + W_BYTES + x_bytes + S_BYTES);
+      tc_fence_after();
+      const uint32_t sw = base + static_cast<uint32_t>(stage) * stage_bytes;
+      const uint32_t sfa = tmem + static_cast<uint32_t>(g.sf_col + slot * SF_COLS);
+      if (++slot == g.sf_slots) slot = 0;
+      const uint32_t sfb = sfa + T * 4;
+      const int steps = min(4, g.ks_total - 4 * kb);
+      const uint64_t da = sf_desc(sw + W_BYTES + x_bytes), db = sf_desc(sw + W_BYTES + x_bytes + S_BYTES);
+      const uint64_t ad = smem_desc_kmajor<128>(sw);
+      const uint64_t bd = smem_desc_kmajor<128>(sw + W_BYTES);
+      if (elect_one()) {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
           cp_sf<1>(sfa + 4 * t, da + 32 * t);
           cp_sf<1>(sfb + 4 * t, db + 32 * t);
         }
-        const uint64_t ad = smem_desc_kmajor<128>(sw);
-        const uint64_t bd = smem_desc_kmajor<128>(sw + W_BYTES);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (k < steps) {
@@ -226,16 +224,18 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
                            sfb + 4 * t, (i > 0 || k > 0) ? 1u : 0u);
           }
         mma_commit(smem_u32(empty + stage));
-        if (++stage == g.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
-      // every MMA issued has completed once this flips
-      mma_commit(smem_u32(accf));
-      volatile int never = 0;
-      pipe::wait(smem_u32(accf), 0, g.wait, &never);
+      __syncwarp();
+      if (++stage == g.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
+    // every MMA issued has completed once this flips
+    if (elect_one()) mma_commit(smem_u32(accf));
+    __syncwarp();
+    volatile int never = 0;
+    pipe::wait(smem_u32(accf), 0, g.wait, &never);
   }
   __syncwarp();
   // ------------------------------------------------------------ epilogue
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
   // consumed stage ring), from where the split's CTAs add their shares.
   const bool ok = pipe::wait(smem_u32(accf), 0, g.wait, abort_flag);
   tc_fence_after();
-  if (warp >= 2 && warp < 6 && __all_sync(0xffffffffu, ok)) {
+  if (warp >= 2 && __all_sync(0xffffffffu, ok)) {
     const int q = warp & 3;
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16);
     for (int c0 = 0; c0 < g.bn; c0 += 16) {
@@ -312,9 +312,8 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
 // its own rows' scale tiles and ALL of the tile's weight scale tiles (each
 // SM's tensor core multiplies its rows with every column, so both tensor
 // memories need every column's scales).
-//   warps 0 and 10..12 producers (one copy per stage each), warp 1 (leader)
-//   scale copies and MMAs, warps 2..9 epilogue, two per TMEM sub-partition on
-//   alternate 32-column chunks.
+//   warp 0 producer, warp 1 (leader) scale copies and MMAs, warps 2..9
+//   epilogue, two per TMEM sub-partition on alternate 32-column chunks.
 template <int BN, bool NV>
 struct CfgP {
   static constexpr int T = f4_tiles(NV);
@@ -336,7 +335,7 @@ struct CfgP {
   static constexpr int SF_COL0 = ACC_BUFS * BN;
   static constexpr int SLOTS_FIT = (512 - SF_COL0) / SF_COLS;
   static constexpr int SLOTS = SLOTS_FIT < STAGES ? SLOTS_FIT : STAGES;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS + 96;   // three more producer warps
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int OFF_SA = STAGES * (A_BYTES + B_BYTES);
   static constexpr int OFF_SB = OFF_SA + STAGES * SA_BYTES;
   static constexpr int OFF_OUT = OFF_SB + STAGES * SB_BYTES;
@@ -414,61 +413,56 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
   griddep_launch_dependents();
   griddep_wait();
 
-  const int prod = warp == 0 ? 0 : warp - (1 + C::EPI_WARPS);   // 0, or 1..3 for the last three warps
-  if (warp == 0 || warp >= 2 + C::EPI_WARPS) {
-    // ------------------------------------------------------------ producers (both CTAs)
-    // A tensor copy holds its issuing thread for some hundred cycles, a stage's
-    // MMAs take 384 - 512: each of the four copies has a thread of its own.
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      const void* const map = prod == 0 ? &tm_a : prod == 1 ? &tm_b : prod == 2 ? &tm_sa : &tm_sb;
-      const uint32_t dst0 = prod == 0 ? sA : prod == 1 ? sB : prod == 2 ? sSA : sSB;
-      const uint32_t step = prod == 0 ? C::A_BYTES : prod == 1 ? C::B_BYTES : prod == 2 ? C::SA_BYTES : C::SB_BYTES;
-      const int dx = prod < 2 ? F4_KB : C::T * 64;
-      for (int t = pair; ok && t < g.num_tiles; t += G) {
-        const int ta = t / g.b_tiles;
-        const int n0 = (t - ta * g.b_tiles) * BN;
-        const int y = prod == 0   ? ta * 256 + static_cast<int>(rank) * 128
-                      : prod == 1 ? n0 + static_cast<int>(rank) * (BN / 2)
-                      : prod == 2 ? ta * 2 + static_cast<int>(rank)
-                                  : n0 / 128;
-        for (int kb = 0; kb < g.kb_total; ++kb) {
-          if (!mbar_wait(smem_u32(empty_bar + stage), phase ^ 1, g.wait, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = smem_u32(full_bar + stage);
-          if (leader && prod == 0) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
-          tma_load_2d_pair(dst0 + static_cast<uint32_t>(stage) * step, map, map_to_rank(fb, 0), kb * dx, y);
-          ++issued;
-          if (++stage == C::STAGES) {
-            stage = 0;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < g.num_tiles; t += G) {
+      const int ta = t / g.b_tiles;
+      const int n0 = (t - ta * g.b_tiles) * BN;
+      for (int kb = 0; kb < g.kb_total; ++kb) {
+        if (!mbar_wait_warp(smem_u32(empty_bar + stage), phase ^ 1, g.wait, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = smem_u32(full_bar + stage);
+        const uint32_t fbl = map_to_rank(fb, 0);
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
+          tma_load_2d_pair(sA + stage * C::A_BYTES, &tm_a, fbl, kb * F4_KB, ta * 256 + static_cast<int>(rank) * 128);
+          tma_load_2d_pair(sB + stage * C::B_BYTES, &tm_b, fbl, kb * F4_KB, n0 + static_cast<int>(rank) * (BN / 2));
+          tma_load_2d_pair(sSA + stage * C::SA_BYTES, &tm_sa, fbl, kb * C::T * 64, ta * 2 + static_cast<int>(rank));
+          tma_load_2d_pair(sSB + stage * C::SB_BYTES, &tm_sb, fbl, kb * C::T * 64, n0 / 128);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) {
+      // Loads already issued land before the CTA leaves (see gemm2sm.cu).
+      if (leader) {
+        WaitCtl quick = g.wait;
+        quick.timeout_ns = quick.timeout_ns < 50000000ull ? quick.timeout_ns : 50000000ull;
+        volatile int never = 0;
+        for (long long i = 0; i < issued && i < C::STAGES; ++i) {
+          if (--stage < 0) {
+            stage = C::STAGES - 1;
             phase ^= 1;
           }
+          mbar_wait(smem_u32(full_bar + stage), phase, quick, &never);
+        }
+      } else {
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 100000ull) {
         }
       }
-      if (!ok) {
-        // Loads already issued land before the CTA leaves (see gemm2sm.cu).
-        if (leader) {
-          WaitCtl quick = g.wait;
-          quick.timeout_ns = quick.timeout_ns < 50000000ull ? quick.timeout_ns : 50000000ull;
-          volatile int never = 0;
-          for (long long i = 0; i < issued && i < C::STAGES; ++i) {
-            if (--stage < 0) {
-              stage = C::STAGES - 1;
-              phase ^= 1;
-            }
-            mbar_wait(smem_u32(full_bar + stage), phase, quick, &never);
-          }
-        } else {
-          const uint64_t t0 = globaltimer();
-          while (globaltimer() - t0 < 100000ull) {
-          }
-        }
-      }
+      __syncwarp();
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
