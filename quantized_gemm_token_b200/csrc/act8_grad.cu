@@ -33,9 +33,10 @@
 namespace dq {
 namespace {
 
-constexpr int WG_THREADS = 448;
+constexpr int WG_GROUPS = 3;                 // converter groups
 constexpr int WG_CVT_WARPS = 4;              // per group
-constexpr int WG_EPI_WARP0 = 10;
+constexpr int WG_EPI_WARP0 = 2 + WG_GROUPS * WG_CVT_WARPS;
+constexpr int WG_THREADS = 32 * (WG_EPI_WARP0 + 4);
 constexpr int WG_STEP = 64;                  // tokens per step
 constexpr int WG_CODES = 128 * WG_STEP;      // bytes: [4 x 16 tokens][128 features][16]
 constexpr int WG_MAX_STAGES = 12;
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     int turn = 0;
     bool ok = true;
     auto advance = [&]() {
-      turn ^= 1;
+      if (++turn == WG_GROUPS) turn = 0;
       if (++stage == g.stages) {
         stage = 0;
         phase ^= 1;
@@ -317,10 +318,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         if (w) {
           const uint32_t s2[2] = {code_scale2(pipe::lds8(sq + WG_CODES + feat)),
                                   code_scale2(pipe::lds8(sq + WG_CODES + 128u + feat))};
+          uint4 c[4];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) c[h] = pipe::lds128(sq + static_cast<uint32_t>(h) * 2048u + feat * 16u);
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            const uint4 c = pipe::lds128(sq + static_cast<uint32_t>(h) * 2048u + feat * 16u);
-            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+            const uint32_t cw[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               r[8 * h + 2 * i] = code_pair(__byte_perm(cw[i], 0u, 0x0100), s2[h >> 1]);
