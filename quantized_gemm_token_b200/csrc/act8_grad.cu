@@ -14,9 +14,15 @@
 //    memory saves its write and the tensor core's read (2 x 16 KB per 64
 //    tokens x 128 features), the bound of the kernels here that build an
 //    operand in shared memory.
-// Roles (448 threads): warp 0 TMA producer; warp 1 MMA issuer; warps 2..9
-// converters, two groups of four taking alternate 64-token steps; warps
-// 10..13 epilogue (lane = feature, column = channel).
+// Roles (five warpgroups): warp 0 TMA producer, warp 1 MMA issuer; two
+// warpgroups of converters taking alternate 64-token steps; two warpgroups of
+// accumulating epilogue warps (lane = feature, a warp holds half of the tile's
+// channels in registers).
+// Sums: the tensor core truncates when it adds to its accumulator, so a chain
+// of MMAs loses about 2^-26 of the sum per instruction, all in one direction
+// (65792 tokens in one chain: 4.4e-5 of the result).  Every 1024 tokens the
+// epilogue adds the accumulator to fp32 registers (rounding to nearest) and
+// the chain starts anew; the eight converted steps in flight cover the read.
 // Few tiles: the tokens are split over a cluster of up to 8 CTAs whose fp32
 // partial tiles are added through distributed shared memory in split order
 // (no workspace, no atomics).
@@ -33,29 +39,33 @@
 namespace dq {
 namespace {
 
-constexpr int WG_GROUPS = 3;                 // converter groups
-constexpr int WG_CVT_WARPS = 4;              // per group
-constexpr int WG_EPI_WARP0 = 2 + WG_GROUPS * WG_CVT_WARPS;
-constexpr int WG_THREADS = 32 * (WG_EPI_WARP0 + 4);
+constexpr int WG_THREADS = 640;
+constexpr int WG_CVT_WARP0 = 4;              // warps 4..11: two converter groups
+constexpr int WG_EPI_WARP0 = 12;             // warps 12..19
+constexpr int WG_EPI_WARPS = 8;
+// registers per thread of the five warpgroups: 40 + 2 * 56 + 2 * 160 = 472, of
+// the 5 * 96 = 480 that the block is launched with; at the end all go back to 96
+constexpr int WG_REGS = 96;
+constexpr int WG_REGS_ISSUE = 40, WG_REGS_CVT = 56, WG_REGS_EPI = 160;
 constexpr int WG_STEP = 64;                  // tokens per step
+constexpr int WG_SEG = 16;                   // steps per accumulator chain
 constexpr int WG_CODES = 128 * WG_STEP;      // bytes: [4 x 16 tokens][128 features][16]
 constexpr int WG_MAX_STAGES = 12;
 constexpr int WG_BAR_BYTES = 512;
-constexpr int WG_OUT_BUF = 4096;             // 32 x 32 fp32, or two 32 x 32 bf16
+constexpr int WG_OUT_BUF = 2048;             // per epilogue warp: 32 x 32 bf16 or 16 x 32 fp32
 constexpr int WG_SLOT_COLS = WG_STEP / 2;    // TMEM columns of one converted step
 constexpr int64_t kGradMaxDim = int64_t(1) << 30;
 
 struct GradArgs {
   int M, N, K;
-  int bn;                  // channels per tile (multiple of 64)
+  int bn;                  // channels per tile (64, 128, 192 or 256)
   int kt, nt;              // feature tiles (128), channel tiles
   int splits, units;
   int ks;                  // token steps: ceil(M / 64)
   int stages;
-  int accs, acc_cols;      // accumulator buffers and their TMEM columns
-  int slots, slot_col;     // converted-step slots and their first column
+  int slots;               // converted-step slots in tensor memory, after the accumulator
   int full_chunks;         // N / 64: chunks the 3-D map covers
-  uint32_t off_out, off_bar;
+  uint32_t off_q, off_e, off_out, off_bar;
   void* dw;
   int f32, accumulate;
   WaitCtl wait;
@@ -100,35 +110,49 @@ __device__ __forceinline__ void tma_add_2d(const void* tmap, uint32_t src, int x
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two bf16 values q * scale from two codes, the bytes at bits 0 and 16 of `u`:
-// 128 + low 7 bits and -128 (-256 for a negative code) are exact bf16 numbers
-// made from the bits, their sum is the code, the product with a power of two
-// is exact.
-__device__ __forceinline__ uint32_t code_pair(uint32_t u, uint32_t s2) {
-  const uint32_t a = (u & 0x007f007fu) | 0x43004300u;
-  const uint32_t b = (u & 0x00800080u) | 0xc300c300u;
-  uint32_t q, r;
-  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(q) : "r"(a), "r"(b));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(q), "r"(s2));
-  return r;
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// 2^(E - 133) twice, NaN for E = 255.
-__device__ __forceinline__ uint32_t code_scale2(uint32_t e) {
-  const uint32_t b = e == 255u ? 0x7fc0u : e >= 7u ? (e - 6u) << 7 : 1u << e;
-  return b | (b << 16);
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A word of four codes -> two pairs of bf16 values q 2^(E - 133).  With v =
+// q + 128 (the code's sign bit flipped), the byte v at the foot of a 16-bit
+// lane IS the bf16 number v 2^-133 (subnormal, or of the least exponent);
+// times 2^127 it is v 2^-6, and fma(v 2^-6, 2^(E - 127), -2^(E - 126)) =
+// (v - 128) 2^(E - 133) exactly.  s2 = 2^(E - 127) and c2 = -2^(E - 126) twice.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t s2, uint32_t c2, uint32_t& r0, uint32_t& r1) {
+  const uint32_t v = w ^ 0x80808080u;
+  const uint32_t u0 = __byte_perm(v, 0u, 0x4140), u1 = __byte_perm(v, 0u, 0x4342);
+  uint32_t t0, t1;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t0) : "r"(u0), "r"(0x7f007f00u));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(t1) : "r"(u1), "r"(0x7f007f00u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r0) : "r"(t0), "r"(s2), "r"(c2));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r1) : "r"(t1), "r"(s2), "r"(c2));
+}
+__device__ __forceinline__ uint32_t code_s2(uint32_t e) { return (e == 0u ? 0x0040u : e << 7) * 0x00010001u; }
+__device__ __forceinline__ uint32_t code_c2(uint32_t e) { return (0x8000u | ((e + 1u) << 7)) * 0x00010001u; }
+// The same for E = 254, whose -2^128 is not a bf16 number (two halves of the
+// scale), and E = 255 (NaN).
+__device__ __forceinline__ void codes4_top(uint32_t w, uint32_t e, uint32_t& r0, uint32_t& r1) {
+  uint32_t a, b;
+  codes4(w, code_s2(253u), code_c2(253u), a, b);
+  const uint32_t two = e == 255u ? 0x7fc07fc0u : 0x40004000u;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r0) : "r"(a), "r"(two));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r1) : "r"(b), "r"(two));
 }
 
 struct GradUnit {
@@ -148,20 +172,19 @@ __device__ __forceinline__ GradUnit grad_unit(const GradArgs& g, int u) {
 __global__ void __launch_bounds__(WG_THREADS, 1)
     act8_grad_kernel(const __grid_constant__ CUtensorMap tm_y3, const __grid_constant__ CUtensorMap tm_y2,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_e,
-                     const __grid_constant__ CUtensorMap tm_c, const GradArgs g) {
+                     const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ GradArgs g) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw);
-  // stage: dY (bn / 64 chunks of 64 tokens x 128 B), codes, scales [2][128]
+  // rings: dY (bn / 64 chunks of 64 tokens x 128 B), codes, scales [2][128]
   const uint32_t y_bytes = static_cast<uint32_t>(g.bn) * 128u;
-  const uint32_t stage_bytes = y_bytes + WG_CODES + 1024u;
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + g.off_bar);
   uint64_t* const cvt = full + WG_MAX_STAGES;
   uint64_t* const empty = cvt + WG_MAX_STAGES;
   uint64_t* const accf = empty + WG_MAX_STAGES;
-  uint64_t* const acce = accf + 2;
-  uint64_t* const drain = acce + 2;
+  uint64_t* const acce = accf + 1;
+  uint64_t* const drain = acce + 1;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -171,13 +194,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     *abort_flag = 0;
     for (int i = 0; i < g.stages; ++i) {
       mbar_init(smem_u32(full + i), 1);
-      mbar_init(smem_u32(cvt + i), WG_CVT_WARPS);
+      mbar_init(smem_u32(cvt + i), 4);
       mbar_init(smem_u32(empty + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(accf + i), 1);
-      mbar_init(smem_u32(acce + i), 4);
-    }
+    mbar_init(smem_u32(accf), 1);
+    mbar_init(smem_u32(acce), WG_EPI_WARPS);
     mbar_init(smem_u32(drain), 1);
     fence_barrier_init();
     tma_prefetch_desc(&tm_y3);
@@ -193,109 +214,115 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
-    int stage = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
-    bool ok = true;
-    const int chunks = g.bn / 64;
-    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
-      const GradUnit t = grad_unit(g, u);
-      const int c0 = t.nt * chunks;
-      // the 3-D map covers whole chunks only: a tile that holds the ragged last one is loaded chunk by chunk
-      const bool whole = c0 + chunks <= g.full_chunks || g.N % 64 == 0;
-      for (int s = t.s0; s < t.s1; ++s) {
-        if (!mbar_wait_warp(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t fb = smem_u32(full + stage);
-        const uint32_t sy = base + static_cast<uint32_t>(stage) * stage_bytes;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(fb, y_bytes + WG_CODES + 256u);
-          tma_load_2d(sy + y_bytes, &tm_q, fb, t.kt * 256, s * 4);
-          tma_load_2d(sy + y_bytes + WG_CODES, &tm_e, fb, t.kt * 128, s * 2);
-          if (whole)
-            tma_load_3d(sy, &tm_y3, fb, 0, s * WG_STEP, c0);
-          else
-            for (int c = 0; c < chunks; ++c)
-              tma_load_2d(sy + static_cast<uint32_t>(c) * 8192u, &tm_y2, fb, (c0 + c) * 64, s * WG_STEP);
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == g.stages) {
-          stage = 0;
-          phase ^= 1;
+  if (warp < WG_CVT_WARP0) {
+    set_regs_down<WG_REGS_ISSUE>();
+    if (warp == 0) {
+      // -------------------------------------------------------- producer
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      const int chunks = g.bn / 64;
+      for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+        const GradUnit t = grad_unit(g, u);
+        const int c0 = t.nt * chunks;
+        // the 3-D map covers whole chunks only: a tile that holds the ragged last one is loaded chunk by chunk
+        const bool whole = c0 + chunks <= g.full_chunks || g.N % 64 == 0;
+        for (int s = t.s0; s < t.s1; ++s) {
+          if (!mbar_wait_warp(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(full + stage);
+          const uint32_t sy = base + static_cast<uint32_t>(stage) * y_bytes;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(fb, y_bytes + WG_CODES + 256u);
+            tma_load_2d(base + g.off_q + static_cast<uint32_t>(stage) * WG_CODES, &tm_q, fb, t.kt * 256, s * 4);
+            tma_load_2d(base + g.off_e + static_cast<uint32_t>(stage) * 256u, &tm_e, fb, t.kt * 128, s * 2);
+            if (whole)
+              tma_load_3d(sy, &tm_y3, fb, 0, s * WG_STEP, c0);
+            else
+              for (int c = 0; c < chunks; ++c)
+                tma_load_2d(sy + static_cast<uint32_t>(c) * 8192u, &tm_y2, fb, (c0 + c) * 64, s * WG_STEP);
+          }
+          __syncwarp();
+          ++issued;
+          if (++stage == g.stages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
-    }
-    volatile int never = 0;
-    for (long long i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
-      pipe::wait(smem_u32(full + static_cast<int>(i % g.stages)), static_cast<uint32_t>((i / g.stages) & 1), g.wait,
-                 &never);
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
-    const uint32_t idesc = idesc_grad(g.bn);
-    int stage = 0, acc = 0, slot = 0;
-    uint32_t phase = 0, aphase = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
-      const GradUnit t = grad_unit(g, u);
-      if (!mbar_wait_warp(smem_u32(acce + acc), aphase ^ 1, g.wait, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + static_cast<uint32_t>(acc * g.acc_cols);
-      for (int s = t.s0; s < t.s1; ++s) {
-        // the converters waited for the copies
-        if (!mbar_wait_warp(smem_u32(cvt + stage), phase, g.wait, abort_flag) ||
-            !mbar_wait_warp(smem_u32(full + stage), phase, g.wait, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t bd = smem_desc_mn(base + static_cast<uint32_t>(stage) * stage_bytes, 8192u);
-        const uint32_t a = tmem + static_cast<uint32_t>(g.slot_col + slot * WG_SLOT_COLS);
-        if (elect_one()) {
+      volatile int never = 0;
+      for (long long i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
+        pipe::wait(smem_u32(full + static_cast<int>(i % g.stages)), static_cast<uint32_t>((i / g.stages) & 1), g.wait,
+                   &never);
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      const uint32_t idesc = idesc_grad(g.bn);
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, aphase = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+        const GradUnit t = grad_unit(g, u);
+        for (int s = t.s0; ok && s < t.s1;) {
+          const int end = min(t.s1, s + WG_SEG);
+          if (!mbar_wait_warp(smem_u32(acce), aphase ^ 1, g.wait, abort_flag)) {
+            ok = false;
+            break;
+          }
+          aphase ^= 1;
+          tc_fence_after();
+          for (int first = s; s < end; ++s) {
+            // the converters waited for the copies
+            if (!mbar_wait_warp(smem_u32(cvt + stage), phase, g.wait, abort_flag) ||
+                !mbar_wait_warp(smem_u32(full + stage), phase, g.wait, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t bd = smem_desc_mn(base + static_cast<uint32_t>(stage) * y_bytes, 8192u);
+            const uint32_t a = tmem + static_cast<uint32_t>(g.bn + slot * WG_SLOT_COLS);
+            if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)        // 16 tokens: 8 columns of A, 2048 bytes of B
-            mma_bf16_ts(d, a + 8 * j, bd + 128 * j, idesc, (s > t.s0 || j > 0) ? 1u : 0u);
-          mma_commit(smem_u32(empty + stage));
-        }
-        __syncwarp();
-        if (++slot == g.slots) slot = 0;
-        if (++stage == g.stages) {
-          stage = 0;
-          phase ^= 1;
+              for (int j = 0; j < 4; ++j)      // 16 tokens: 8 columns of A, 2048 bytes of B
+                mma_bf16_ts(tmem, a + 8 * j, bd + 128 * j, idesc, (s > first || j > 0) ? 1u : 0u);
+              mma_commit(smem_u32(empty + stage));
+            }
+            __syncwarp();
+            if (++slot == g.slots) slot = 0;
+            if (++stage == g.stages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+          if (elect_one()) mma_commit(smem_u32(accf));
+          __syncwarp();
         }
       }
-      if (!ok) break;
-      if (elect_one()) mma_commit(smem_u32(accf + acc));
+      if (elect_one()) mma_commit(smem_u32(drain));
       __syncwarp();
-      if (++acc == g.accs) {
-        acc = 0;
-        aphase ^= 1;
-      }
+      volatile int never = 0;
+      pipe::wait(smem_u32(drain), 0, g.wait, &never);
     }
-    if (elect_one()) mma_commit(smem_u32(drain));
-    __syncwarp();
-    volatile int never = 0;
-    pipe::wait(smem_u32(drain), 0, g.wait, &never);
   } else if (warp < WG_EPI_WARP0) {
     // ---------------------------------------------------------- converters
-    const int grp = (warp - 2) >> 2;
+    set_regs_down<WG_REGS_CVT>();
+    const int grp = (warp - WG_CVT_WARP0) >> 2;
     const int q = warp & 3;                      // TMEM sub-partition
     const uint32_t feat = static_cast<uint32_t>(q * 32 + lane);
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g.slot_col);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g.bn);
     int stage = 0, slot = 0, old = 0;            // ring positions of the CTA's current step, over its units
     uint32_t phase = 0, old_phase = 0;
     int warm = g.slots;                          // steps until a slot is used again
     int turn = 0;
     bool ok = true;
     auto advance = [&]() {
-      if (++turn == WG_GROUPS) turn = 0;
+      turn ^= 1;
       if (++stage == g.stages) {
         stage = 0;
         phase ^= 1;
@@ -312,33 +339,32 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       const GradUnit t = grad_unit(g, u);
       for (int s = t.s0; s < t.s1; ++s, advance()) {
         if (turn != grp) continue;
+        // the step's copies have landed, its slot's previous MMAs completed
         bool w = pipe::wait(smem_u32(full + stage), phase, g.wait, abort_flag);
-        const uint32_t sq = base + static_cast<uint32_t>(stage) * stage_bytes + y_bytes;
-        uint32_t r[32];
-        if (w) {
-          const uint32_t s2[2] = {code_scale2(pipe::lds8(sq + WG_CODES + feat)),
-                                  code_scale2(pipe::lds8(sq + WG_CODES + 128u + feat))};
-          uint4 c[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) c[h] = pipe::lds128(sq + static_cast<uint32_t>(h) * 2048u + feat * 16u);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const uint32_t cw[4] = {c[h].x, c[h].y, c[h].z, c[h].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              r[8 * h + 2 * i] = code_pair(__byte_perm(cw[i], 0u, 0x0100), s2[h >> 1]);
-              r[8 * h + 2 * i + 1] = code_pair(__byte_perm(cw[i], 0u, 0x0302), s2[h >> 1]);
-            }
-          }
-          // the slot's previous MMAs have completed
-          if (warm == 0) w = pipe::wait(smem_u32(empty + old), old_phase, g.wait, abort_flag);
-        }
+        if (w && warm == 0) w = pipe::wait(smem_u32(empty + old), old_phase, g.wait, abort_flag);
         if (!__all_sync(0xffffffffu, w)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        tmem_st_32x32b_x32(lane_base + static_cast<uint32_t>(slot) * WG_SLOT_COLS, r);
+        const uint32_t sq = base + g.off_q + static_cast<uint32_t>(stage) * WG_CODES + feat * 16u;
+        const uint32_t se = base + g.off_e + static_cast<uint32_t>(stage) * 256u + feat;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {            // 32 tokens with one scale
+          const uint32_t e = pipe::lds8(se + 128u * b);
+          const uint4 c0 = pipe::lds128(sq + 4096u * b), c1 = pipe::lds128(sq + 4096u * b + 2048u);
+          const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          uint32_t r[16];
+          const uint32_t s2 = code_s2(e), c2 = code_c2(e);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) codes4(cw[i], s2, c2, r[2 * i], r[2 * i + 1]);
+          if (e >= 254u) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) codes4_top(cw[i], e, r[2 * i], r[2 * i + 1]);
+          }
+          __syncwarp();
+          tmem_st_32x32b_x16(lane_base + static_cast<uint32_t>(slot * WG_SLOT_COLS + 16 * b), r);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -346,77 +372,103 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       }
     }
   } else {
-    // ---------------------------------------------------------- epilogue
+    // ---------------------------------------------------------- accumulation and epilogue
+    set_regs_up<WG_REGS_EPI>();
+    const int ew = warp - WG_EPI_WARP0;
     const int q = warp & 3;
-    const uint32_t buf0 = base + g.off_out + static_cast<uint32_t>(warp - WG_EPI_WARP0) * WG_OUT_BUF;
-    int acc = 0, flip = 0;
+    const int half = g.bn / 2;                   // channels of this warp: [h0, h0 + half) of the tile
+    const int h0 = (ew >> 2) * half;
+    const uint32_t buf = base + g.off_out + static_cast<uint32_t>(ew) * WG_OUT_BUF;
+    const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h0);
     uint32_t aphase = 0;
-    for (int u = blockIdx.x; u < g.units; u += gridDim.x) {
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const GradUnit t = grad_unit(g, u);
-      const bool w = pipe::wait(smem_u32(accf + acc), aphase, g.wait, abort_flag);
-      if (!__all_sync(0xffffffffu, w)) break;
-      tc_fence_after();
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * g.acc_cols);
-      const int k0 = t.kt * 128 + q * 32;
-      const int n0 = t.nt * g.bn;
-#pragma unroll 1
-      for (int c0 = 0; c0 < g.bn; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tb + c0, r);
-        tmem_ld_wait();
-        if (c0 + 32 == g.bn) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(acce + acc));
-        }
-        if (g.splits > 1) {
-          // fp32 partial [channel][feature] at the start of the stage ring (the CTA's only unit: all consumed)
+      float sum[128];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            pipe::sts32(base + static_cast<uint32_t>((c0 + j) * 128 + q * 32 + lane) * 4u, r[j]);
-          continue;
+      for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+      for (int s = t.s0; s < t.s1; s += WG_SEG) {
+        const bool w = pipe::wait(smem_u32(accf), aphase, g.wait, abort_flag);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
         }
-        uint32_t buf = buf0;
-        if (g.f32) {
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
-          // row j = channel, 128 bytes of features, 16-byte units XORed with j mod 8 (the map's 128B swizzle)
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            pipe::sts32(buf + static_cast<uint32_t>(j * 128 + (((lane >> 2) ^ (j & 7)) << 4) + (lane & 3) * 4), r[j]);
-        } else {
-          buf += static_cast<uint32_t>(flip) * (WG_OUT_BUF / 2);
-          flip ^= 1;
-          if (lane == 0) bulk_wait_group_read<1>();
-          __syncwarp();
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-          pipe::stage_bf16_pairs(buf, pk, 32, lane);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (k0 < g.K && n0 + c0 < g.N) {            // blocks wholly outside are not issued
-            if (g.f32 && g.accumulate) tma_add_2d(&tm_c, buf, k0, n0 + c0);
-            else tma_store_2d(&tm_c, buf, g.f32 ? k0 : 2 * k0, n0 + c0);
-          }
-          bulk_commit_group();
-        }
-      }
-      if (++acc == g.accs) {
-        acc = 0;
         aphase ^= 1;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (16 * c < half) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(tb + 16 * c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[16 * c + j] += __uint_as_float(r[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(acce));
+      }
+      if (!ok) break;
+      const int k0 = t.kt * 128 + q * 32;
+      const int n0 = t.nt * g.bn + h0;
+      if (g.splits > 1) {
+        // fp32 partial [channel][feature] over the rings (the CTA's only unit: its last accumulator is
+        // complete, so every stage has been consumed)
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+          if (j < half)
+            pipe::sts32(base + static_cast<uint32_t>((h0 + j) * 128 + q * 32 + lane) * 4u, __float_as_uint(sum[j]));
+        continue;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {              // 16 channels at a time
+        if (16 * c < half) {
+          const bool issue = g.f32 || (c & 1);   // bf16 blocks hold 32 channels
+          if (g.f32 || !(c & 1)) {
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+          }
+          if (g.f32) {
+            // row j = channel, 128 bytes of features, 16-byte units XORed with j mod 8 (the map's 128B swizzle)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              pipe::sts32(buf + static_cast<uint32_t>(j * 128 + (((lane >> 2) ^ (j & 7)) << 4) + (lane & 3) * 4),
+                          __float_as_uint(sum[16 * c + j]));
+          } else {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pk[i] = pack_bf16x2(sum[16 * c + 2 * i], sum[16 * c + 2 * i + 1]);
+#pragma unroll
+            for (int i = 8; i < 16; ++i) pk[i] = 0u;
+            pipe::stage_bf16_pairs(buf + (c & 1) * 1024u, pk, 16, lane);
+          }
+          if (issue) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int n = n0 + (g.f32 ? 16 * c : 16 * (c - 1));
+              if (k0 < g.K && n < g.N) {         // blocks wholly outside are not issued
+                if (g.f32 && g.accumulate) tma_add_2d(&tm_c, buf, k0, n);
+                else tma_store_2d(&tm_c, buf, g.f32 ? k0 : 2 * k0, n);
+                bulk_commit_group();
+              }
+            }
+          }
+        }
       }
     }
     if (lane == 0) bulk_wait_group<0>();
-    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Every thread takes its launch share of the registers again, but not before
+  // all roles have ended: a warp that grew earlier (one without a role would
+  // at once) could take what the epilogue's own growth still waits for.
+  if (warp < WG_EPI_WARP0) set_regs_up<WG_REGS>();
+  else set_regs_down<WG_REGS>();
   if (warp == 1) tmem_dealloc(tmem, 512);
 
   if (g.splits > 1) {
@@ -584,26 +636,40 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
   g.M = static_cast<int>(M);
   g.N = static_cast<int>(N);
   g.K = static_cast<int>(K);
-  g.bn = N > 128 ? 192 : N > 64 ? 128 : 64;
   g.kt = static_cast<int>((K + 127) / 128);
-  g.nt = static_cast<int>((N + g.bn - 1) / g.bn);
   g.ks = static_cast<int>((M + WG_STEP - 1) / WG_STEP);
-  const int64_t tiles = static_cast<int64_t>(g.kt) * g.nt;
+  // Tile width and split with the least estimated time: waves of steps, a step
+  // costing about 0.25 + bn / 1280 us, plus a few us per unit for its ends.
+  int64_t tiles = 0;
+  double best = 1e300;
+  for (int bn = 64; bn <= 256; bn += 64) {
+    const int64_t nt = (N + bn - 1) / bn, n = nt * g.kt;
+    for (int sp = 1; sp <= 8; sp *= 2) {
+      if (sp > 1 && (n * sp > dev->sm_count || g.ks < 2 * sp)) break;
+      const double waves = static_cast<double>((n * sp + dev->sm_count - 1) / dev->sm_count);
+      const double cost = waves * (((g.ks + sp - 1) / sp) * (0.25 + bn / 1280.0) + 2.0) + (sp > 1 ? 1.0 + 0.2 * sp : 0.0);
+      if (cost < best) {
+        best = cost;
+        g.bn = bn;
+        g.nt = static_cast<int>(nt);
+        g.splits = sp;
+        tiles = n;
+      }
+    }
+  }
   if (tiles > 0x3fffffff) return DQ_ERR_UNSUPPORTED;
-  g.splits = 1;
-  while (g.splits < 8 && tiles * g.splits * 2 <= dev->sm_count && g.ks >= 4 * g.splits) g.splits *= 2;
   g.units = static_cast<int>(tiles) * g.splits;
-  g.accs = 2;
-  g.acc_cols = g.bn;
-  g.slot_col = 2 * g.bn;
-  g.slots = std::min(8, (512 - g.slot_col) / WG_SLOT_COLS);
   g.full_chunks = static_cast<int>(N / 64);
-  const int stage_bytes = g.bn * 128 + WG_CODES + 1024;
-  const int fixed = 1024 + 4 * WG_OUT_BUF + WG_BAR_BYTES;
+  const int stage_bytes = g.bn * 128 + WG_CODES + 256;
+  const int fixed = 2048 + WG_EPI_WARPS * WG_OUT_BUF + WG_BAR_BYTES;
   g.stages = std::min(WG_MAX_STAGES, (227 * 1024 - fixed) / stage_bytes);
-  g.slots = std::min(g.slots, g.stages);   // a slot's wait looks back less than one lap of the ring
-  g.off_out = static_cast<uint32_t>(g.stages * stage_bytes);
-  g.off_bar = g.off_out + 4 * WG_OUT_BUF;
+  // a slot's wait looks back less than one lap of the ring
+  g.slots = std::min((512 - g.bn) / WG_SLOT_COLS, g.stages);
+  g.off_q = static_cast<uint32_t>(g.stages * g.bn * 128);
+  g.off_e = g.off_q + static_cast<uint32_t>(g.stages * WG_CODES);
+  // (the swizzle of the output blocks counts from 1024-byte boundaries)
+  g.off_out = (g.off_e + static_cast<uint32_t>(g.stages * 256) + 1023u) & ~1023u;
+  g.off_bar = g.off_out + WG_EPI_WARPS * WG_OUT_BUF;
   const int smem = static_cast<int>(g.off_bar) + WG_BAR_BYTES + 1024;
   g.dw = dw;
   g.f32 = f32;
@@ -624,7 +690,7 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
     return st;
   if ((st = make_tmap_2d(&te, CU_TENSOR_MAP_DATA_TYPE_UINT8, scales, K, groups, K, 128, 2, 0)) != DQ_OK) return st;
   if (f32) {
-    st = make_tmap_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dw, K, N, static_cast<uint64_t>(K) * 4, 32, 32, 128);
+    st = make_tmap_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dw, K, N, static_cast<uint64_t>(K) * 4, 32, 16, 128);
   } else {
     st = make_tmap_2d(&tc, CU_TENSOR_MAP_DATA_TYPE_UINT8, dw, static_cast<uint64_t>(K) * 2, N,
                       static_cast<uint64_t>(K) * 2, 64, 32, 0);
