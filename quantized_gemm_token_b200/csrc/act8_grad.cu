@@ -14,10 +14,15 @@
 //    memory saves its write and the tensor core's read (2 x 16 KB per 64
 //    tokens x 128 features), the bound of the kernels here that build an
 //    operand in shared memory.
-// Roles (five warpgroups): warp 0 TMA producer, warp 1 MMA issuer; two
-// warpgroups of converters taking alternate 64-token steps; two warpgroups of
-// accumulating epilogue warps (lane = feature, a warp holds half of the tile's
-// channels in registers).
+// Roles (five warpgroups): warp 0 dY producer, warp 1 MMA issuer, warp 2 code
+// producer; two warpgroups of converters taking alternate 64-token steps; two
+// warpgroups of accumulating epilogue warps (lane = feature, a warp holds half
+// of the tile's channels in registers).
+// Three rings, each as deep as its own round trip asks: dY in shared memory
+// (freed by the MMAs), codes in shared memory (freed by the converters), and
+// converted steps in tensor memory.  With one ring for both loads a step's
+// slot waited for copy, conversion AND product in turn (0.34 us per step with
+// neither arithmetic nor MMAs in it).
 // Sums: the tensor core truncates when it adds to its accumulator, so a chain
 // of MMAs loses about 2^-26 of the sum per instruction, all in one direction
 // (65792 tokens in one chain: 4.4e-5 of the result).  Every 1024 tokens the
@@ -50,7 +55,8 @@ constexpr int WG_REGS_ISSUE = 40, WG_REGS_CVT = 56, WG_REGS_EPI = 160;
 constexpr int WG_STEP = 64;                  // tokens per step
 constexpr int WG_SEG = 16;                   // steps per accumulator chain
 constexpr int WG_CODES = 128 * WG_STEP;      // bytes: [4 x 16 tokens][128 features][16]
-constexpr int WG_MAX_STAGES = 12;
+constexpr int WG_MAX_RING = 8;               // stages or slots of each ring
+constexpr int WG_CODE_STAGE = WG_CODES + 256;
 constexpr int WG_BAR_BYTES = 512;
 constexpr int WG_OUT_BUF = 2048;             // per epilogue warp: 32 x 32 bf16 or 16 x 32 fp32
 constexpr int WG_SLOT_COLS = WG_STEP / 2;    // TMEM columns of one converted step
@@ -62,10 +68,10 @@ struct GradArgs {
   int kt, nt;              // feature tiles (128), channel tiles
   int splits, units;
   int ks;                  // token steps: ceil(M / 64)
-  int stages;
+  int stages, code_stages; // dY and code rings
   int slots;               // converted-step slots in tensor memory, after the accumulator
   int full_chunks;         // N / 64: chunks the 3-D map covers
-  uint32_t off_q, off_e, off_out, off_bar;
+  uint32_t off_q, off_out, off_bar;
   void* dw;
   int f32, accumulate;
   WaitCtl wait;
@@ -177,12 +183,15 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw);
-  // rings: dY (bn / 64 chunks of 64 tokens x 128 B), codes, scales [2][128]
+  // rings: dY (bn / 64 chunks of 64 tokens x 128 B); codes, then their scales [2][128]
   const uint32_t y_bytes = static_cast<uint32_t>(g.bn) * 128u;
-  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + g.off_bar);
-  uint64_t* const cvt = full + WG_MAX_STAGES;
-  uint64_t* const empty = cvt + WG_MAX_STAGES;
-  uint64_t* const accf = empty + WG_MAX_STAGES;
+  uint64_t* const yfull = reinterpret_cast<uint64_t*>(smem + g.off_bar);
+  uint64_t* const yempty = yfull + WG_MAX_RING;
+  uint64_t* const qfull = yempty + WG_MAX_RING;
+  uint64_t* const qempty = qfull + WG_MAX_RING;
+  uint64_t* const afull = qempty + WG_MAX_RING;    // a slot holds a converted step
+  uint64_t* const aempty = afull + WG_MAX_RING;
+  uint64_t* const accf = aempty + WG_MAX_RING;
   uint64_t* const acce = accf + 1;
   uint64_t* const drain = acce + 1;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -192,10 +201,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < g.stages; ++i) {
-      mbar_init(smem_u32(full + i), 1);
-      mbar_init(smem_u32(cvt + i), 4);
-      mbar_init(smem_u32(empty + i), 1);
+    for (int i = 0; i < WG_MAX_RING; ++i) {
+      mbar_init(smem_u32(yfull + i), 1);
+      mbar_init(smem_u32(yempty + i), 1);
+      mbar_init(smem_u32(qfull + i), 1);
+      mbar_init(smem_u32(qempty + i), 4);
+      mbar_init(smem_u32(afull + i), 4);
+      mbar_init(smem_u32(aempty + i), 1);
     }
     mbar_init(smem_u32(accf), 1);
     mbar_init(smem_u32(acce), WG_EPI_WARPS);
@@ -219,8 +231,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 
   if (warp < WG_CVT_WARP0) {
     set_regs_down<WG_REGS_ISSUE>();
-    if (warp == 0) {
-      // -------------------------------------------------------- producer
+    if (warp == 0 || warp == 2) {
+      // -------------------------------------------------------- producers
+      const bool codes = warp == 2;
+      uint64_t* const full = codes ? qfull : yfull;
+      uint64_t* const empty = codes ? qempty : yempty;
+      const int ring = codes ? g.code_stages : g.stages;
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
@@ -238,34 +254,39 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
           }
           const uint32_t fb = smem_u32(full + stage);
           const uint32_t sy = base + static_cast<uint32_t>(stage) * y_bytes;
+          const uint32_t sq = base + g.off_q + static_cast<uint32_t>(stage) * WG_CODE_STAGE;
           if (elect_one()) {
-            mbar_arrive_expect_tx(fb, y_bytes + WG_CODES + 256u);
-            tma_load_2d(base + g.off_q + static_cast<uint32_t>(stage) * WG_CODES, &tm_q, fb, t.kt * 256, s * 4);
-            tma_load_2d(base + g.off_e + static_cast<uint32_t>(stage) * 256u, &tm_e, fb, t.kt * 128, s * 2);
-            if (whole)
-              tma_load_3d(sy, &tm_y3, fb, 0, s * WG_STEP, c0);
-            else
-              for (int c = 0; c < chunks; ++c)
-                tma_load_2d(sy + static_cast<uint32_t>(c) * 8192u, &tm_y2, fb, (c0 + c) * 64, s * WG_STEP);
+            if (codes) {
+              mbar_arrive_expect_tx(fb, WG_CODE_STAGE);
+              tma_load_2d(sq, &tm_q, fb, t.kt * 256, s * 4);
+              tma_load_2d(sq + WG_CODES, &tm_e, fb, t.kt * 128, s * 2);
+            } else {
+              mbar_arrive_expect_tx(fb, y_bytes);
+              if (whole)
+                tma_load_3d(sy, &tm_y3, fb, 0, s * WG_STEP, c0);
+              else
+                for (int c = 0; c < chunks; ++c)
+                  tma_load_2d(sy + static_cast<uint32_t>(c) * 8192u, &tm_y2, fb, (c0 + c) * 64, s * WG_STEP);
+            }
           }
           __syncwarp();
           ++issued;
-          if (++stage == g.stages) {
+          if (++stage == ring) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
+      // every copy issued lands before the CTA can exit
       volatile int never = 0;
-      for (long long i = issued > g.stages ? issued - g.stages : 0; i < issued; ++i)
-        pipe::wait(smem_u32(full + static_cast<int>(i % g.stages)), static_cast<uint32_t>((i / g.stages) & 1), g.wait,
-                   &never);
+      for (long long i = issued > ring ? issued - ring : 0; i < issued; ++i)
+        pipe::wait(smem_u32(full + static_cast<int>(i % ring)), static_cast<uint32_t>((i / ring) & 1), g.wait, &never);
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       const uint32_t idesc = idesc_grad(g.bn);
       int stage = 0, slot = 0;
-      uint32_t phase = 0, aphase = 0;
-      bool ok = true;
+      uint32_t phase = 0, sphase = 0, aphase = 0;
+      bool ok = true, tested = false;             // tested: the next step's operands were found ready
       for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
         const GradUnit t = grad_unit(g, u);
         for (int s = t.s0; ok && s < t.s1;) {
@@ -277,27 +298,33 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
           aphase ^= 1;
           tc_fence_after();
           for (int first = s; s < end; ++s) {
-            // the converters waited for the copies
-            if (!mbar_wait_warp(smem_u32(cvt + stage), phase, g.wait, abort_flag) ||
-                !mbar_wait_warp(smem_u32(full + stage), phase, g.wait, abort_flag)) {
+            if (!mbar_wait_warp2(tested, smem_u32(yfull + stage), phase, smem_u32(afull + slot), sphase, g.wait,
+                                 abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint64_t bd = smem_desc_mn(base + static_cast<uint32_t>(stage) * y_bytes, 8192u);
             const uint32_t a = tmem + static_cast<uint32_t>(g.bn + slot * WG_SLOT_COLS);
-            if (elect_one()) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)      // 16 tokens: 8 columns of A, 2048 bytes of B
-                mma_bf16_ts(tmem, a + 8 * j, bd + 128 * j, idesc, (s > first || j > 0) ? 1u : 0u);
-              mma_commit(smem_u32(empty + stage));
+            const uint32_t yb = smem_u32(yempty + stage), ab = smem_u32(aempty + slot);
+            if (++slot == g.slots) {
+              slot = 0;
+              sphase ^= 1;
             }
-            __syncwarp();
-            if (++slot == g.slots) slot = 0;
             if (++stage == g.stages) {
               stage = 0;
               phase ^= 1;
             }
+            const bool ty = mbar_test(smem_u32(yfull + stage), phase), ta = mbar_test(smem_u32(afull + slot), sphase);
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)      // 16 tokens: 8 columns of A, 2048 bytes of B
+                mma_bf16_ts(tmem, a + 8 * j, bd + 128 * j, idesc, (s > first || j > 0) ? 1u : 0u);
+              mma_commit(yb);
+              mma_commit(ab);
+            }
+            __syncwarp();
+            tested = ty && ta;
           }
           if (!ok) break;
           if (elect_one()) mma_commit(smem_u32(accf));
@@ -316,39 +343,35 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     const int q = warp & 3;                      // TMEM sub-partition
     const uint32_t feat = static_cast<uint32_t>(q * 32 + lane);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g.bn);
-    int stage = 0, slot = 0, old = 0;            // ring positions of the CTA's current step, over its units
-    uint32_t phase = 0, old_phase = 0;
-    int warm = g.slots;                          // steps until a slot is used again
+    int stage = 0, slot = 0;                     // ring positions of the CTA's current step, over its units
+    uint32_t phase = 0, sphase = 0;
     int turn = 0;
     bool ok = true;
     auto advance = [&]() {
       turn ^= 1;
-      if (++stage == g.stages) {
+      if (++stage == g.code_stages) {
         stage = 0;
         phase ^= 1;
       }
-      if (++slot == g.slots) slot = 0;
-      if (warm > 0) {
-        --warm;
-      } else if (++old == g.stages) {
-        old = 0;
-        old_phase ^= 1;
+      if (++slot == g.slots) {
+        slot = 0;
+        sphase ^= 1;
       }
     };
     for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
       const GradUnit t = grad_unit(g, u);
       for (int s = t.s0; s < t.s1; ++s, advance()) {
         if (turn != grp) continue;
-        // the step's copies have landed, its slot's previous MMAs completed
-        bool w = pipe::wait(smem_u32(full + stage), phase, g.wait, abort_flag);
-        if (w && warm == 0) w = pipe::wait(smem_u32(empty + old), old_phase, g.wait, abort_flag);
-        if (!__all_sync(0xffffffffu, w)) {
+        // the step's codes have landed, its slot's previous MMAs completed
+        const bool tq = mbar_test(smem_u32(qfull + stage), phase), ta = mbar_test(smem_u32(aempty + slot), sphase ^ 1);
+        if (!mbar_wait_warp2(tq && ta, smem_u32(qfull + stage), phase, smem_u32(aempty + slot), sphase ^ 1, g.wait,
+                             abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t sq = base + g.off_q + static_cast<uint32_t>(stage) * WG_CODES + feat * 16u;
-        const uint32_t se = base + g.off_e + static_cast<uint32_t>(stage) * 256u + feat;
+        const uint32_t sq = base + g.off_q + static_cast<uint32_t>(stage) * WG_CODE_STAGE + feat * 16u;
+        const uint32_t se = base + g.off_q + static_cast<uint32_t>(stage) * WG_CODE_STAGE + WG_CODES + feat;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {            // 32 tokens with one scale
           const uint32_t e = pipe::lds8(se + 128u * b);
@@ -365,10 +388,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
           __syncwarp();
           tmem_st_32x32b_x16(lane_base + static_cast<uint32_t>(slot * WG_SLOT_COLS + 16 * b), r);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(qempty + stage));   // the codes are in registers
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(cvt + stage));
+        if (lane == 0) mbar_arrive(smem_u32(afull + slot));
       }
     }
   } else {
@@ -388,8 +413,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
       for (int s = t.s0; s < t.s1; s += WG_SEG) {
-        const bool w = pipe::wait(smem_u32(accf), aphase, g.wait, abort_flag);
-        if (!__all_sync(0xffffffffu, w)) {
+        if (!mbar_wait_warp(smem_u32(accf), aphase, g.wait, abort_flag)) {
           ok = false;
           break;
         }
@@ -413,7 +437,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       const int k0 = t.kt * 128 + q * 32;
       const int n0 = t.nt * g.bn + h0;
       if (g.splits > 1) {
-        // fp32 partial [channel][feature] over the rings (the CTA's only unit: its last accumulator is
+        // fp32 partial [channel][feature] over the dY ring (the CTA's only unit: its last accumulator is
         // complete, so every stage has been consumed)
 #pragma unroll
         for (int j = 0; j < 128; ++j)
@@ -660,16 +684,19 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
   if (tiles > 0x3fffffff) return DQ_ERR_UNSUPPORTED;
   g.units = static_cast<int>(tiles) * g.splits;
   g.full_chunks = static_cast<int>(N / 64);
-  const int stage_bytes = g.bn * 128 + WG_CODES + 256;
-  const int fixed = 2048 + WG_EPI_WARPS * WG_OUT_BUF + WG_BAR_BYTES;
-  g.stages = std::min(WG_MAX_STAGES, (227 * 1024 - fixed) / stage_bytes);
-  // a slot's wait looks back less than one lap of the ring
-  g.slots = std::min((512 - g.bn) / WG_SLOT_COLS, g.stages);
-  g.off_q = static_cast<uint32_t>(g.stages * g.bn * 128);
-  g.off_e = g.off_q + static_cast<uint32_t>(g.stages * WG_CODES);
+  // Five stages of dY at 256 channels, the rest of the shared memory for codes.
+  // The rings that the two converter groups share have an even length, so that
+  // a stage belongs to one group: a parity wait cannot tell a lap from the one
+  // two before it, and a group that ran ahead of the other could take its
+  // stage's next lap for landed.
+  const int room = 227 * 1024 - 1024 - WG_EPI_WARPS * WG_OUT_BUF - WG_BAR_BYTES;
+  g.stages = std::min(WG_MAX_RING, (room - 6 * WG_CODE_STAGE) / (g.bn * 128));
+  g.code_stages = std::min(WG_MAX_RING, (room - g.stages * g.bn * 128) / WG_CODE_STAGE) & ~1;
+  g.slots = std::min(WG_MAX_RING, (512 - g.bn) / WG_SLOT_COLS) & ~1;
   // (the swizzle of the output blocks counts from 1024-byte boundaries)
-  g.off_out = (g.off_e + static_cast<uint32_t>(g.stages * 256) + 1023u) & ~1023u;
-  g.off_bar = g.off_out + WG_EPI_WARPS * WG_OUT_BUF;
+  g.off_out = static_cast<uint32_t>(g.stages * g.bn * 128);
+  g.off_q = g.off_out + WG_EPI_WARPS * WG_OUT_BUF;
+  g.off_bar = g.off_q + static_cast<uint32_t>(g.code_stages * WG_CODE_STAGE);
   const int smem = static_cast<int>(g.off_bar) + WG_BAR_BYTES + 1024;
   g.dw = dw;
   g.f32 = f32;
