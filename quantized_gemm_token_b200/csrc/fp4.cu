@@ -418,30 +418,33 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     long long issued = 0;
-    bool ok = true;
+    bool ok = true, tested = true;       // tested: the next stage was found free
     for (int t = pair; ok && t < g.num_tiles; t += G) {
       const int ta = t / g.b_tiles;
       const int n0 = (t - ta * g.b_tiles) * BN;
       for (int kb = 0; kb < g.kb_total; ++kb) {
-        if (!mbar_wait_warp(smem_u32(empty_bar + stage), phase ^ 1, g.wait, abort_flag)) {
+        if (!tested && !mbar_wait_warp(smem_u32(empty_bar + stage), phase ^ 1, g.wait, abort_flag)) {
           ok = false;
           break;
         }
         const uint32_t fb = smem_u32(full_bar + stage);
         const uint32_t fbl = map_to_rank(fb, 0);
-        if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
-          tma_load_2d_pair(sA + stage * C::A_BYTES, &tm_a, fbl, kb * F4_KB, ta * 256 + static_cast<int>(rank) * 128);
-          tma_load_2d_pair(sB + stage * C::B_BYTES, &tm_b, fbl, kb * F4_KB, n0 + static_cast<int>(rank) * (BN / 2));
-          tma_load_2d_pair(sSA + stage * C::SA_BYTES, &tm_sa, fbl, kb * C::T * 64, ta * 2 + static_cast<int>(rank));
-          tma_load_2d_pair(sSB + stage * C::SB_BYTES, &tm_sb, fbl, kb * C::T * 64, n0 / 128);
-        }
-        __syncwarp();
+        const int now = stage;
         ++issued;
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1;
         }
+        const bool te = mbar_test(smem_u32(empty_bar + stage), phase ^ 1);
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
+          tma_load_2d_pair(sA + now * C::A_BYTES, &tm_a, fbl, kb * F4_KB, ta * 256 + static_cast<int>(rank) * 128);
+          tma_load_2d_pair(sB + now * C::B_BYTES, &tm_b, fbl, kb * F4_KB, n0 + static_cast<int>(rank) * (BN / 2));
+          tma_load_2d_pair(sSA + now * C::SA_BYTES, &tm_sa, fbl, kb * C::T * 64, ta * 2 + static_cast<int>(rank));
+          tma_load_2d_pair(sSB + now * C::SB_BYTES, &tm_sb, fbl, kb * C::T * 64, n0 / 128);
+        }
+        __syncwarp();
+        tested = __all_sync(0xffffffffu, te);
       }
     }
     if (!ok) {
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
       int warm = C::SLOTS;                // stages until a slot is used again
       int old = 0;                        // stage (and its lap's parity) that used the slot before
       uint32_t old_phase = 0;
-      bool ok = true;
+      bool ok = true, tested = false;     // tested: the next stage (and its slot) was found ready
       const int ks_total = (g.K + 63) / 64;
       for (int t = pair; ok && t < g.num_tiles; t += G) {
         // an odd tile of width 192 (or 64) starts in the middle of a scale row block
@@ -482,32 +485,36 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kb = 0; kb < g.kb_total; ++kb) {
-          if (!mbar_wait_warp(smem_u32(full_bar + stage), phase, g.wait, abort_flag)) {
+          // the stage has landed and, once the slots have been used, the
+          // MMAs that read this scale slot before have completed
+          const bool reuse = C::SLOTS < C::STAGES && warm == 0;
+          if (!tested && !(mbar_wait_warp(smem_u32(full_bar + stage), phase, g.wait, abort_flag) &&
+                           (!reuse || mbar_wait_warp(smem_u32(empty_bar + old), old_phase, g.wait, abort_flag)))) {
             ok = false;
             break;
           }
-          if (C::SLOTS < C::STAGES) {
-            if (warm > 0) {
-              --warm;
-            } else {                      // the scale slot's previous user has completed
-              if (!mbar_wait_warp(smem_u32(empty_bar + old), old_phase, g.wait, abort_flag)) {
-                ok = false;
-                break;
-              }
-              if (++old == C::STAGES) {
-                old = 0;
-                old_phase ^= 1;
-              }
-            }
-          }
           tc_fence_after();
           const uint32_t sfa = tmem_base + C::SF_COL0 + static_cast<uint32_t>(slot) * C::SF_COLS;
-          if (++slot == C::SLOTS) slot = 0;
           const uint32_t sfb = sfa + C::SF_A;
           const uint64_t da = sf_desc(sSA + stage * C::SA_BYTES), db = sf_desc(sSB + stage * C::SB_BYTES);
           const uint64_t ad = smem_desc_kmajor<128>(sA + stage * C::A_BYTES);
           const uint64_t bd = smem_desc_kmajor<128>(sB + stage * C::B_BYTES);
+          const uint32_t eb = smem_u32(empty_bar + stage);
           const int steps = min(4, ks_total - 4 * kb);
+          if (++slot == C::SLOTS) slot = 0;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+          if (warm > 0) {
+            --warm;
+          } else if (++old == C::STAGES) {
+            old = 0;
+            old_phase ^= 1;
+          }
+          // the next stage's barriers are tested before this stage's MMAs are issued
+          const bool tf = mbar_test(smem_u32(full_bar + stage), phase);
+          const bool to = C::SLOTS == C::STAGES || warm > 0 || mbar_test(smem_u32(empty_bar + old), old_phase);
           if (elect_one()) {
 #pragma unroll
             for (int s = 0; s < C::T; ++s) {
@@ -522,13 +529,10 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
                 mma_fp4<2, NV>(d, ad + 2 * k, bd + 2 * k, idesc_fp4(256, BN, NV, NV ? 0 : k & 1), sfa + 4 * s,
                                sfb + 4 * C::RB * s + col_b, (kb > 0 || k > 0) ? 1u : 0u);
               }
-            mma_commit_pair_both(smem_u32(empty_bar + stage));
+            mma_commit_pair_both(eb);
           }
           __syncwarp();
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+          tested = __all_sync(0xffffffffu, tf && to);
         }
         if (!ok) break;
         if (elect_one()) mma_commit_pair_both(smem_u32(accf_bar + acc));
