@@ -307,34 +307,33 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- many tokens
-// A pair of SMs per 256 x BN tile (cta_group::2), as the int8 pair kernel:
+// A pair of SMs per 256 x 256 (or narrower) tile (cta_group::2), as the int8 pair kernel:
 // each CTA loads its 128 token rows and half of the tile's weight rows, plus
 // its own rows' scale tiles and ALL of the tile's weight scale tiles (each
 // SM's tensor core multiplies its rows with every column, so both tensor
 // memories need every column's scales).
 //   warp 0 producer, warp 1 (leader) scale copies and MMAs, warps 2..9
 //   epilogue, two per TMEM sub-partition on alternate 32-column chunks.
-template <int BN, bool NV>
+template <bool NV>
 struct CfgP {
+  static constexpr int BN = 256;
   static constexpr int T = f4_tiles(NV);
-  static constexpr int RB = (BN + 127) / 128;           // weight scale row blocks of a tile
+  static constexpr int RB = 2;                          // weight scale row blocks of a tile
   static constexpr int A_BYTES = 128 * F4_KB;
   static constexpr int B_BYTES = (BN / 2) * F4_KB;
   static constexpr int SA_BYTES = T * 512;
   static constexpr int SB_BYTES = RB * T * 512;
   static constexpr int CTA_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static constexpr int EPI_WARPS = 8;
+  static constexpr int CHUNKS = BN / 32 / (EPI_WARPS / 4);   // 32-column chunks per epilogue warp
   static constexpr int OUT_BUF_BYTES = 32 * 32 * 4;
   static constexpr int OUT_BYTES = EPI_WARPS * OUT_BUF_BYTES;
   static constexpr int BAR_BYTES = 512;
   static constexpr int SLACK = 1024;
   static constexpr int STAGES = (227 * 1024 - SLACK - BAR_BYTES - OUT_BYTES - kScSlotBytes) / CTA_BYTES;
-  static constexpr int ACC_BUFS = BN <= 192 ? 2 : 1;
   static constexpr int SF_A = T * 4, SF_B = T * RB * 4; // scale columns per stage
   static constexpr int SF_COLS = SF_A + SF_B;
-  static constexpr int SF_COL0 = ACC_BUFS * BN;
-  static constexpr int SLOTS_FIT = (512 - SF_COL0) / SF_COLS;
-  static constexpr int SLOTS = SLOTS_FIT < STAGES ? SLOTS_FIT : STAGES;
+  static constexpr int SF_COL0 = BN;                    // after the accumulator
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int OFF_SA = STAGES * (A_BYTES + B_BYTES);
   static constexpr int OFF_SB = OFF_SA + STAGES * SA_BYTES;
@@ -342,17 +341,19 @@ struct CfgP {
   static constexpr int OFF_SC = OFF_OUT + OUT_BYTES;
   static constexpr int OFF_BARS = OFF_SC + kScSlotBytes;
   static constexpr int SMEM_BYTES = OFF_BARS + BAR_BYTES + SLACK;
-  static_assert(STAGES >= 3 && SLOTS >= 2 && SMEM_BYTES <= 227 * 1024, "resources");
-  static_assert((2 * STAGES + 2 * ACC_BUFS + 3) * 8 + 8 <= BAR_BYTES, "barrier area");
-  static_assert(BN % 64 == 0 && BN <= 256, "tile width: a scale row block or half of one");
+  static_assert(STAGES >= 3 && SMEM_BYTES <= 227 * 1024, "shared memory");
+  // every stage has a scale slot of its own, so a slot is free when its stage is
+  static_assert(SF_COL0 + STAGES * SF_COLS <= 512, "tensor memory");
+  static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
 };
 
-template <int BN, bool NV>
-__global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
+template <bool NV>
+__global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                    const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
-                    const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ GemmArgs g) {
-  using C = CfgP<BN, NV>;
+                    const __grid_constant__ CUtensorMap tm_b2, const __grid_constant__ CUtensorMap tm_sa,
+                    const __grid_constant__ CUtensorMap tm_sb, const __grid_constant__ CUtensorMap tm_c,
+                    const __grid_constant__ GemmArgs g) {
+  using C = CfgP<NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* empty_bar = full_bar + C::STAGES;
   uint64_t* accf_bar = empty_bar + C::STAGES;
-  uint64_t* acce_bar = accf_bar + C::ACC_BUFS;
-  uint64_t* drain_bar = acce_bar + C::ACC_BUFS;
+  uint64_t* acce_bar = accf_bar + 1;
+  uint64_t* drain_bar = acce_bar + 1;
   uint64_t* sc_full = drain_bar + 1;
   uint64_t* sc_free = sc_full + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sc_free + 1);
@@ -385,16 +386,15 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
       mbar_init(smem_u32(full_bar + s), 1);
       mbar_init(smem_u32(empty_bar + s), 1);
     }
-    for (int a = 0; a < C::ACC_BUFS; ++a) {
-      mbar_init(smem_u32(accf_bar + a), 1);
-      mbar_init(smem_u32(acce_bar + a), 2 * C::EPI_WARPS);
-    }
+    mbar_init(smem_u32(accf_bar), 1);
+    mbar_init(smem_u32(acce_bar), 2 * C::EPI_WARPS);
     mbar_init(smem_u32(drain_bar), 1);
     mbar_init(smem_u32(sc_full), 1);
     mbar_init(smem_u32(sc_free), C::EPI_WARPS);
     fence_barrier_init();
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_b2);
     tma_prefetch_desc(&tm_sa);
     tma_prefetch_desc(&tm_sb);
     tma_prefetch_desc(&tm_c);
@@ -420,8 +420,10 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
     long long issued = 0;
     bool ok = true, tested = true;       // tested: the next stage was found free
     for (int t = pair; ok && t < g.num_tiles; t += G) {
-      const int ta = t / g.b_tiles;
-      const int n0 = (t - ta * g.b_tiles) * BN;
+      const TileGeom geo = tile_geom(g, t, C::BN, true);
+      const int ta = geo.ta, n0 = geo.n0, half = geo.width / 2;
+      const uint32_t stage_tx = 2u * static_cast<uint32_t>(C::CTA_BYTES - C::B_BYTES + half * F4_KB);
+      const void* const tmb = geo.narrow ? &tm_b2 : &tm_b;
       for (int kb = 0; kb < g.kb_total; ++kb) {
         if (!tested && !mbar_wait_warp(smem_u32(empty_bar + stage), phase ^ 1, g.wait, abort_flag)) {
           ok = false;
@@ -437,9 +439,9 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
         }
         const bool te = mbar_test(smem_u32(empty_bar + stage), phase ^ 1);
         if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(fb, 2u * C::CTA_BYTES);
+          if (leader) mbar_arrive_expect_tx(fb, stage_tx);
           tma_load_2d_pair(sA + now * C::A_BYTES, &tm_a, fbl, kb * F4_KB, ta * 256 + static_cast<int>(rank) * 128);
-          tma_load_2d_pair(sB + now * C::B_BYTES, &tm_b, fbl, kb * F4_KB, n0 + static_cast<int>(rank) * (BN / 2));
+          tma_load_2d_pair(sB + now * C::B_BYTES, tmb, fbl, kb * F4_KB, n0 + static_cast<int>(rank) * half);
           tma_load_2d_pair(sSA + now * C::SA_BYTES, &tm_sa, fbl, kb * C::T * 64, ta * 2 + static_cast<int>(rank));
           tma_load_2d_pair(sSB + now * C::SB_BYTES, &tm_sb, fbl, kb * C::T * 64, n0 / 128);
         }
@@ -470,51 +472,37 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (leader) {
-      int stage = 0, acc = 0;
+      int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
-      int slot = 0;                       // scale slot of this stage
-      int warm = C::SLOTS;                // stages until a slot is used again
-      int old = 0;                        // stage (and its lap's parity) that used the slot before
-      uint32_t old_phase = 0;
-      bool ok = true, tested = false;     // tested: the next stage (and its slot) was found ready
+      bool ok = true, tested = false;     // tested: the next stage was found landed
       const int ks_total = (g.K + 63) / 64;
       for (int t = pair; ok && t < g.num_tiles; t += G) {
-        // an odd tile of width 192 (or 64) starts in the middle of a scale row block
-        const uint32_t col_b = static_cast<uint32_t>((((t % g.b_tiles) * BN) % 128) / 32);
-        if (!mbar_wait_warp(smem_u32(acce_bar + acc), acc_phase ^ 1, g.wait, abort_flag)) break;
+        const TileGeom geo = tile_geom(g, t, C::BN, true);
+        // a tile may start in the middle of a scale row block (widths of 64 and 192)
+        const uint32_t col_b = static_cast<uint32_t>((geo.n0 % 128) / 32);
+        const uint32_t id0 = idesc_fp4(256, geo.width, NV, 0), id1 = NV ? id0 : idesc_fp4(256, geo.width, NV, 1);
+        if (!mbar_wait_warp(smem_u32(acce_bar), acc_phase ^ 1, g.wait, abort_flag)) break;
+        acc_phase ^= 1;
         tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(acc * BN);
         for (int kb = 0; kb < g.kb_total; ++kb) {
-          // the stage has landed and, once the slots have been used, the
-          // MMAs that read this scale slot before have completed
-          const bool reuse = C::SLOTS < C::STAGES && warm == 0;
-          if (!tested && !(mbar_wait_warp(smem_u32(full_bar + stage), phase, g.wait, abort_flag) &&
-                           (!reuse || mbar_wait_warp(smem_u32(empty_bar + old), old_phase, g.wait, abort_flag)))) {
+          if (!tested && !mbar_wait_warp(smem_u32(full_bar + stage), phase, g.wait, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sfa = tmem_base + C::SF_COL0 + static_cast<uint32_t>(slot) * C::SF_COLS;
+          const uint32_t sfa = tmem_base + C::SF_COL0 + static_cast<uint32_t>(stage) * C::SF_COLS;
           const uint32_t sfb = sfa + C::SF_A;
           const uint64_t da = sf_desc(sSA + stage * C::SA_BYTES), db = sf_desc(sSB + stage * C::SB_BYTES);
           const uint64_t ad = smem_desc_kmajor<128>(sA + stage * C::A_BYTES);
           const uint64_t bd = smem_desc_kmajor<128>(sB + stage * C::B_BYTES);
           const uint32_t eb = smem_u32(empty_bar + stage);
           const int steps = min(4, ks_total - 4 * kb);
-          if (++slot == C::SLOTS) slot = 0;
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1;
           }
-          if (warm > 0) {
-            --warm;
-          } else if (++old == C::STAGES) {
-            old = 0;
-            old_phase ^= 1;
-          }
-          // the next stage's barriers are tested before this stage's MMAs are issued
+          // the next stage's barrier is tested before this stage's MMAs are issued
           const bool tf = mbar_test(smem_u32(full_bar + stage), phase);
-          const bool to = C::SLOTS == C::STAGES || warm > 0 || mbar_test(smem_u32(empty_bar + old), old_phase);
           if (elect_one()) {
 #pragma unroll
             for (int s = 0; s < C::T; ++s) {
@@ -526,21 +514,17 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
             for (int k = 0; k < 4; ++k)
               if (k < steps) {
                 const int s = NV ? k : k >> 1;
-                mma_fp4<2, NV>(d, ad + 2 * k, bd + 2 * k, idesc_fp4(256, BN, NV, NV ? 0 : k & 1), sfa + 4 * s,
+                mma_fp4<2, NV>(tmem_base, ad + 2 * k, bd + 2 * k, (k & 1) ? id1 : id0, sfa + 4 * s,
                                sfb + 4 * C::RB * s + col_b, (kb > 0 || k > 0) ? 1u : 0u);
               }
             mma_commit_pair_both(eb);
           }
           __syncwarp();
-          tested = __all_sync(0xffffffffu, tf && to);
+          tested = __all_sync(0xffffffffu, tf);
         }
         if (!ok) break;
-        if (elect_one()) mma_commit_pair_both(smem_u32(accf_bar + acc));
+        if (elect_one()) mma_commit_pair_both(smem_u32(accf_bar));
         __syncwarp();
-        if (++acc == C::ACC_BUFS) {
-          acc = 0;
-          acc_phase ^= 1;
-        }
       }
       if (elect_one()) mma_commit_pair(map_to_rank(smem_u32(drain_bar), 0));
       __syncwarp();
@@ -569,57 +553,50 @@ __global__ void __launch_bounds__(CfgP<BN, NV>::THREADS, 1)
       out_flip ^= 1;
       return b;
     };
-    int acc = 0;
     uint32_t acc_phase = 0;
     uint32_t sc_phase = 0;
     for (int t = pair; t < g.num_tiles; t += G) {
-      const int ta = t / g.b_tiles;
-      const int n0 = (t - ta * g.b_tiles) * BN;
-      const int m_slab = ta * 256 + static_cast<int>(rank) * 128 + sp * 32;
+      const TileGeom geo = tile_geom(g, t, C::BN, true);
+      const int n0 = geo.n0, nch = geo.width / 32;
+      const int m_slab = geo.ta * 256 + static_cast<int>(rank) * 128 + sp * 32;
       const int m = m_slab + lane;
       if (ep_tid == 0) {
         if (t != pair && !mbar_wait(smem_u32(sc_free), sc_phase ^ 1, g.wait, abort_flag)) break;
         // the tile's column scales (unless there are none) and bias
-        const int ncols = min(BN, g.N - n0);
-        const uint32_t sb = !g.out_s32 && g.s_col != nullptr ? static_cast<uint32_t>(ncols) * 4u : 0u;
-        const uint32_t bb = !g.out_s32 && g.bias != nullptr ? static_cast<uint32_t>(ncols) * 2u : 0u;
+        const int ncols = min(geo.width, g.N - n0);
+        const uint32_t sb = !g.out_s32 && g.s_col != nullptr && ncols > 0 ? static_cast<uint32_t>(ncols) * 4u : 0u;
+        const uint32_t bb = !g.out_s32 && g.bias != nullptr && ncols > 0 ? static_cast<uint32_t>(ncols) * 2u : 0u;
         mbar_arrive_expect_tx(smem_u32(sc_full), sb + bb);
         if (sb) bulk_load_1d(sc_slot, g.s_col + n0, sb, smem_u32(sc_full));
         if (bb) bulk_load_1d(sc_slot + kScBiasOff, g.bias + n0, bb, smem_u32(sc_full));
       }
       const float srow = (!g.out_s32 && g.s_row != nullptr && m < g.M) ? __ldg(g.s_row + m) : 1.0f;
-      if (!mbar_wait(smem_u32(accf_bar + acc), acc_phase, g.wait, abort_flag)) break;
+      if (!mbar_wait(smem_u32(accf_bar), acc_phase, g.wait, abort_flag)) break;
       if (!mbar_wait(smem_u32(sc_full), sc_phase, g.wait, abort_flag)) break;
+      acc_phase ^= 1;
       sc_phase ^= 1;
       tc_fence_after();
-      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(sp * 32) << 16) + static_cast<uint32_t>(acc * BN);
-      constexpr int NCH = BN / 32;
-      const int last_c = grp + ((NCH - 1 - grp) / GROUPS) * GROUPS;
-#pragma unroll 1
-      for (int c0 = grp; c0 < NCH; c0 += 2 * GROUPS) {
-        uint32_t r[2][32];
-        const bool two = c0 + GROUPS < NCH;
-        tmem_ld_32x32b_x32(tbase + c0 * 32, r[0]);
-        if (two) tmem_ld_32x32b_x32(tbase + (c0 + GROUPS) * 32, r[1]);
-        tmem_ld_wait();
-        if (c0 == last_c || (two && c0 + GROUPS == last_c)) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(acce_bar + acc), 0));
-        }
+      // The one accumulator (256 columns leave tensor memory only for the
+      // scales beside it) is taken into registers whole and handed back before
+      // any of it is scaled and stored, so the next tile's MMAs wait for the
+      // reads alone.
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(sp * 32) << 16);
+      uint32_t r[C::CHUNKS][32];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = c0 + i * GROUPS;
-          if (i == 1 && !two) break;
+      for (int i = 0; i < C::CHUNKS; ++i)
+        if (grp + i * GROUPS < nch) tmem_ld_32x32b_x32(tbase + (grp + i * GROUPS) * 32, r[i]);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(acce_bar), 0));
+#pragma unroll
+      for (int i = 0; i < C::CHUNKS; ++i) {
+        const int c = grp + i * GROUPS;
+        if (c < nch)
           store_row_chunk_staged<true>(g, &tm_c, next_buf(), lane, m_slab, n0 + c * 32, r[i], srow, sc_slot, c * 32);
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(sc_free));
-      if (++acc == C::ACC_BUFS) {
-        acc = 0;
-        acc_phase ^= 1;
-      }
     }
     if (lane == 0) bulk_wait_group<0>();
     __syncwarp();
@@ -698,29 +675,73 @@ dq_status launch_few(const uint8_t* A, const uint8_t* sfa, int64_t M, int64_t K,
   return e == cudaSuccess ? DQ_OK : cuda_fail(e);
 }
 
-template <int BN, bool NV>
+// Tiles for `pairs` CTA pairs: 256 columns wide, or all of one narrower
+// width, or whole waves of 256 and the rest in one wave of a narrower width;
+// whichever takes the fewest stage times.  A stage's time follows the bytes
+// that a CTA loads for it (the bound: 38.9 KB at 256 columns against 512 cycles
+// of MMAs), a tile's ends cost about 2.5 stages.
+struct PairPlan {
+  int t1, bn2, mb0, c_start, first_cnt, per_row, num_tiles;
+};
+bool plan_pair(int64_t M, int64_t N, int kb_total, int64_t pairs, PairPlan& out) {
+  const int64_t at = (M + 255) / 256, bt = (N + 255) / 256, T = at * bt;
+  if (T > 0x3fffff) return false;                    // (64 columns: at most four times as many)
+  auto cost = [&](int w) { return kb_total * (0.51 + 0.49 * w / 256) + 2.5 * w / 256; };
+  double best = static_cast<double>((T + pairs - 1) / pairs) * cost(256);
+  out = PairPlan{static_cast<int>(T), 0, 0, 0, 0, 0, static_cast<int>(T)};
+  for (int w = 192; w >= 64; w -= 64) {
+    const int64_t row = (N + w - 1) / w, n = at * row;
+    const double c = static_cast<double>((n + pairs - 1) / pairs) * cost(w);
+    if (c < 0.98 * best) {
+      best = c;
+      out = PairPlan{0, w, 0, 0, static_cast<int>(row), static_cast<int>(row), static_cast<int>(n)};
+    }
+    const int64_t t1 = T / pairs * pairs;            // whole waves
+    if (t1 == 0 || t1 == T) continue;
+    const int64_t mb0 = t1 / bt, c0 = (t1 % bt) * 256;
+    const int64_t first = (N - c0 + w - 1) / w, t2 = first + (at - mb0 - 1) * row;
+    if (t2 > pairs) continue;
+    const double c2 = static_cast<double>(t1 / pairs) * cost(256) + cost(w);
+    if (c2 < 0.98 * best) {
+      best = c2;
+      out = PairPlan{static_cast<int>(t1), w, static_cast<int>(mb0), static_cast<int>(c0), static_cast<int>(first),
+                     static_cast<int>(row), static_cast<int>(t1 + t2)};
+    }
+  }
+  return true;
+}
+
+template <bool NV>
 dq_status launch_pair(const uint8_t* A, const uint8_t* sfa, const uint8_t* W, const uint8_t* sfw, GemmArgs g, int pairs,
                       cudaStream_t stream) {
-  using C = CfgP<BN, NV>;
+  using C = CfgP<NV>;
   const int64_t K = g.K;
   const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
   g.a_tiles = (g.M + 255) / 256;
-  g.b_tiles = (g.N + BN - 1) / BN;
+  g.b_tiles = (g.N + C::BN - 1) / C::BN;
   g.kb_total = static_cast<int>((K + F4_KE - 1) / F4_KE);
-  const int64_t tiles = static_cast<int64_t>(g.a_tiles) * g.b_tiles;
-  if (tiles > 0x3fffffff) return DQ_ERR_UNSUPPORTED;
-  g.num_tiles = static_cast<int>(tiles);
-  CUtensorMap ta, tb, tsa, tsb, tc;
+  PairPlan p;
+  if (!plan_pair(g.M, g.N, g.kb_total, pairs, p)) return DQ_ERR_UNSUPPORTED;
+  g.t1 = p.t1;
+  g.bn2 = p.bn2;
+  g.mb0 = p.mb0;
+  g.c_start = p.c_start;
+  g.first_cnt = p.first_cnt;
+  g.per_row = p.per_row;
+  g.num_tiles = p.num_tiles;
+  CUtensorMap ta, tb, tb2, tsa, tsb, tc;
   dq_status st;
   if ((st = make_tmap_u8_2d(&ta, A, K / 2, g.M, K / 2, F4_KB, 128, 128)) != DQ_OK) return st;
-  if ((st = make_tmap_u8_2d(&tb, W, K / 2, g.N, K / 2, F4_KB, BN / 2, 128)) != DQ_OK) return st;
+  if ((st = make_tmap_u8_2d(&tb, W, K / 2, g.N, K / 2, F4_KB, C::BN / 2, 128)) != DQ_OK) return st;
+  tb2 = tb;
+  if (g.bn2 > 0 && (st = make_tmap_u8_2d(&tb2, W, K / 2, g.N, K / 2, F4_KB, g.bn2 / 2, 128)) != DQ_OK) return st;
   if ((st = make_tmap_sf(&tsa, sfa, (g.M + 127) / 128, atoms, C::T, 1)) != DQ_OK) return st;
   if ((st = make_tmap_sf(&tsb, sfw, (g.N + 127) / 128, atoms, C::T, C::RB)) != DQ_OK) return st;
   if ((st = make_tmap_out_2d(&tc, g.out, g.N, g.M, g.out_s32 ? 4 : 2)) != DQ_OK) return st;
-  auto k = fp4_pair_kernel<BN, NV>;
+  auto k = fp4_pair_kernel<NV>;
   if ((st = smem_limit_once(reinterpret_cast<const void*>(k), C::SMEM_BYTES)) != DQ_OK) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(pairs, tiles)));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, g.num_tiles)));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = stream;
@@ -733,7 +754,7 @@ dq_status launch_pair(const uint8_t* A, const uint8_t* sfa, const uint8_t* W, co
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ta, tb, tsa, tsb, tc, g);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, ta, tb, tb2, tsa, tsb, tc, g);
   return e == cudaSuccess ? DQ_OK : cuda_fail(e);
 }
 
@@ -787,7 +808,7 @@ dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float* s_row
   g.wait = wait;
   int pairs = 0;
   if ((st = pair_slots(*d, &pairs)) != DQ_OK) return st;
-  return nv ? launch_pair<192, true>(A, sfa, W, sfw, g, pairs, cs) : launch_pair<192, false>(A, sfa, W, sfw, g, pairs, cs);
+  return nv ? launch_pair<true>(A, sfa, W, sfw, g, pairs, cs) : launch_pair<false>(A, sfa, W, sfw, g, pairs, cs);
 }
 
 }  // extern "C"

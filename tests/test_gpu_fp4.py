@@ -198,7 +198,7 @@ def test_few_tokens(M, N, K, fmt):
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("M,N,K", [(257, 8, 32), (257, 192, 256), (300, 384, 1056), (512, 1160, 544), (700, 136, 2080),
-                                   (1024, 2048, 736), (1799, 1280, 1280)])
+                                   (1024, 2048, 736), (1799, 1280, 1280), (2300, 4104, 288), (2048, 4096, 4096)])
 def test_many_tokens(M, N, K, fmt):
     _check_product(M, N, K, fmt, bias=M % 2 == 1, seed=M)
 
