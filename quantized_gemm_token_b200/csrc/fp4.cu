@@ -91,8 +91,8 @@ struct FewArgs {
   int M, N;
   int ks_total;            // 64-feature MMA steps: ceil(K / 64)
   int kb_total;            // stages: ceil(K / 256)
-  int bn;                  // tokens per tile (multiple of 16, <= 128)
-  int nt, tt, splits;      // channel tiles, token tiles, feature splits
+  int bn;                  // token columns (M rounded up to 16, <= 64)
+  int nt, splits;          // channel tiles, feature splits
   int stages;
   int tmem_cols, sf_col;   // allocation; first column of the scale slots
   int sf_slots;            // tensor-memory scale slots
@@ -154,12 +154,9 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
   griddep_launch_dependents();
   griddep_wait();
 
-  // unit: (channel tile, token tile, split), splits neighbouring (one cluster)
-  const int u = blockIdx.x;
-  const int split = u % g.splits;
-  const int tile = u / g.splits;
-  const int nt = tile / g.tt;
-  const int tt = tile - nt * g.tt;
+  // unit: (channel tile, split), splits neighbouring (one cluster)
+  const int nt = blockIdx.x / g.splits;
+  const int split = blockIdx.x - nt * g.splits;
   const int kb0 = static_cast<int>(static_cast<int64_t>(split) * g.kb_total / g.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(split + 1) * g.kb_total / g.splits);
 
@@ -175,8 +172,8 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
         mbar_arrive_expect_tx(fb, stage_bytes);
         tma_load_2d(sw, &tm_w, fb, kb * F4_KB, nt * 128);
         tma_load_2d(sw + W_BYTES + x_bytes, &tm_sw, fb, kb * T * 64, nt);
-        tma_load_2d(sw + W_BYTES, &tm_x, fb, kb * F4_KB, tt * g.bn);
-        tma_load_2d(sw + W_BYTES + x_bytes + S_BYTES, &tm_sx, fb, kb * T * 64, tt * g.bn / 128);
+        tma_load_2d(sw + W_BYTES, &tm_x, fb, kb * F4_KB, 0);
+        tma_load_2d(sw + W_BYTES + x_bytes + S_BYTES, &tm_sx, fb, kb * T * 64, 0);
       }
       __syncwarp();
       ++issued;
@@ -264,12 +261,11 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
   const int r0 = split * rows;
   const int r1 = min(g.bn, r0 + rows);
   for (int i = threadIdx.x; i < (r1 - r0) * 32; i += FS_THREADS) {
-    const int tok = r0 + (i >> 5);
+    const int m = r0 + (i >> 5);
     const int quad = i & 31;
-    const int m = tt * g.bn + tok;
     const int ch = nt * 128 + 4 * quad;
     if (m >= g.M || ch >= g.N) continue;              // N % 8 == 0: the quad is all in or all out
-    const uint32_t off = base + static_cast<uint32_t>(tok * 128 + 4 * quad) * 4u;
+    const uint32_t off = base + static_cast<uint32_t>(m * 128 + 4 * quad) * 4u;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (g.splits > 1) {
       for (int sp = 0; sp < g.splits; ++sp) {
@@ -618,26 +614,27 @@ dq_status make_tmap_sf(CUtensorMap* map, const uint8_t* sf, int64_t row_blocks, 
                       static_cast<uint32_t>(tiles) * 64, static_cast<uint32_t>(box_rows), 0);
 }
 
+// Two CTAs per SM.  All units resident at once share the memory's bandwidth
+// evenly and end together, whatever their number per SM, so only too few of
+// them call for a split.
+int few_splits(int nt, int kb_total, int sm_count) {
+  int splits = 1;
+  while (splits < 8 && nt * splits <= sm_count && kb_total / (2 * splits) >= 2) splits *= 2;
+  return splits;
+}
+
 template <bool NV>
 dq_status launch_few(const uint8_t* A, const uint8_t* sfa, int64_t M, int64_t K, const uint8_t* W, const uint8_t* sfw,
                      int64_t N, FewArgs g, int sm_count, cudaStream_t stream) {
   constexpr int T = f4_tiles(NV);
   const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
-  g.bn = M >= 128 ? 128 : static_cast<int>((M + 15) / 16 * 16);
-  g.tt = static_cast<int>((M + g.bn - 1) / g.bn);
+  g.bn = static_cast<int>((M + 15) / 16 * 16);
   g.nt = static_cast<int>((N + 127) / 128);
   g.kb_total = static_cast<int>((K + F4_KE - 1) / F4_KE);
   g.ks_total = static_cast<int>((K + 63) / 64);
-  // Two CTAs per SM.  All units resident at once share the memory's bandwidth
-  // evenly and end together, whatever their number per SM, so only too few of
-  // them call for a split.
-  const int per_sm = 2;
-  const int64_t tiles = static_cast<int64_t>(g.nt) * g.tt;
-  g.splits = 1;
-  while (g.splits < 8 && tiles * g.splits * 2 <= static_cast<int64_t>(per_sm) * sm_count && g.kb_total / (2 * g.splits) >= 2)
-    g.splits *= 2;
+  g.splits = few_splits(g.nt, g.kb_total, sm_count);
   const int stage_bytes = 128 * F4_KB + g.bn * F4_KB + 2 * T * 512;
-  const int limit = (227 * 1024 - per_sm * 1024) / per_sm;
+  const int limit = (227 * 1024 - 2 * 1024) / 2;      // two CTAs per SM
   g.stages = (limit - 1024 - FS_BAR_BYTES) / stage_bytes;
   const int max_need = (g.kb_total + g.splits - 1) / g.splits;
   g.stages = std::min({g.stages, FS_MAX_STAGES, max_need});
@@ -646,8 +643,8 @@ dq_status launch_few(const uint8_t* A, const uint8_t* sfa, int64_t M, int64_t K,
   g.off_bar = static_cast<uint32_t>((ring + 15) / 16 * 16);
   const int smem = static_cast<int>(g.off_bar) + FS_BAR_BYTES + 1024;
   constexpr int SF_COLS = 2 * T * 4;
-  g.sf_col = g.bn <= 32 ? 32 : g.bn <= 64 ? 64 : 128;
-  g.tmem_cols = g.sf_col == 128 ? 256 : 128;
+  g.sf_col = g.bn <= 32 ? 32 : 64;
+  g.tmem_cols = 128;
   g.sf_slots = std::min((g.tmem_cols - g.sf_col) / SF_COLS, g.stages);
   CUtensorMap tw, tx, tsw, tsx;
   dq_status st;
@@ -658,7 +655,7 @@ dq_status launch_few(const uint8_t* A, const uint8_t* sfa, int64_t M, int64_t K,
   auto k = fp4_few_kernel<NV>;
   if ((st = smem_limit_once(reinterpret_cast<const void*>(k), smem)) != DQ_OK) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(g.nt * g.splits));
   cfg.blockDim = dim3(FS_THREADS);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
@@ -783,7 +780,12 @@ dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float* s_row
   const auto cs = reinterpret_cast<cudaStream_t>(stream);
   const bool nv = fmt == DQ_FP4_NV;
   const WaitCtl wait{d->err_word, wait_timeout_ns()};
-  if (M <= 256) {
+  // Few tokens: up to 32, or 64 without a split (K = 8192, N = 28672: 24.2,
+  // 25.7, 27.7 and 32.0 us at 1, 32, 64 and 128 tokens against the pair
+  // kernel's 44.6, 31.0, 31.9 and 33.1; K = N = 4096, split eight ways: 6.2,
+  // 7.5, 9.9 and 13.8 against 11.4, 9.4, 8.6 and 8.8).
+  const int nt = static_cast<int>((N + 127) / 128);
+  if (M <= 32 || (M <= 64 && few_splits(nt, static_cast<int>((K + F4_KE - 1) / F4_KE), d->sm_count) == 1)) {
     FewArgs f = {};
     f.M = static_cast<int>(M);
     f.N = static_cast<int>(N);
