@@ -127,13 +127,19 @@ def _check(status: int, where: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# The current stream's handle without building a torch.cuda.Stream (10 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _stream_obj(stream) -> torch.cuda.Stream:
@@ -672,23 +678,49 @@ def _fp4_scale_shape(rows: int, K: int, code: int):
     return ((rows + 127) // 128, (K + g - 1) // g, 512)
 
 
-def _same_device(first: torch.Tensor, **others):
-    """Every tensor of a call on one device, and that device the current one
-    (a kernel is launched on the current device)."""
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name}: on {t.device}, expected {first.device}")
+def _here(t: torch.Tensor, name: str) -> int:
+    """The device index of a call's first tensor, which must be the current
+    device (a kernel is launched there)."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _rows(x: torch.Tensor, name: str) -> int:
-    """Row stride of a [rows, width] tensor with contiguous rows."""
-    if x.shape[1] != 1 and x.stride(1) != 1:
+def _arg(t, dtype, shape, dev: int, name: str):
+    """A contiguous tensor of the given type and shape on device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _rows(x: torch.Tensor, dtype, name: str):
+    """(rows, width, row stride) of a 2-D tensor with contiguous rows that do
+    not overlap."""
+    if x.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dims, got {x.dim()}")
+    R, C = x.shape
+    ld, step = x.stride()
+    if step != 1 and C != 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    if x.shape[0] > 1 and x.stride(0) < x.shape[1]:
-        raise ValueError(f"{name}: rows must not overlap")
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+    if ld < C:
+        if R > 1:
+            raise ValueError(f"{name}: rows must not overlap")
+        ld = C
+    return R, C, ld
 
 
 def dq_fp4_scales_size(rows: int, K: int, fmt="nv") -> int:
@@ -698,32 +730,30 @@ def dq_fp4_scales_size(rows: int, K: int, fmt="nv") -> int:
 
 def _quantize_fp4(fn, name, x, dtype, fmt, q, sf, s, stream):
     code = _fp4_fmt(fmt)
-    _need(x, dtype, "x", 2)
-    ld = _rows(x, "x")
-    M, K = x.shape
+    dev = _here(x, "x")
+    M, K, ld = _rows(x, dtype, "x")
     if K < 1 or K % 32 != 0:
         raise ValueError(f"x: the row length must be a positive multiple of 32, got {K}")
     shape = _fp4_scale_shape(M, K, code)
+    ldq = K // 2
     if q is None:
-        q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        q = x.new_empty((M, K // 2), dtype=torch.uint8)
+    else:
+        if _here(q, "q") != dev or _rows(q, torch.uint8, "q")[:2] != (M, K // 2):
+            raise ValueError(f"q must be {(M, K // 2)}")
+        ldq = _rows(q, torch.uint8, "q")[2]
     if sf is None:
-        sf = torch.empty(shape, dtype=torch.uint8, device=x.device)
-    if s is None and code == DQ_FP4_NV:
-        s = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _need(q, torch.uint8, "q", 2)
-    _need(sf, torch.uint8, "sf", 3)
-    _contig(sf, "sf")
-    if tuple(q.shape) != (M, K // 2) or tuple(sf.shape) != shape:
-        raise ValueError(f"q must be {(M, K // 2)} and sf {shape}")
+        sf = x.new_empty(shape, dtype=torch.uint8)
+    else:
+        _arg(sf, torch.uint8, shape, dev, "sf")
     if code == DQ_FP4_NV:
-        _need(s, torch.float32, "row scales", 1)
-        _contig(s, "row scales")
-        if s.numel() != M:
-            raise ValueError("row scales: one per row")
+        if s is None:
+            s = x.new_empty((M,), dtype=torch.float32)
+        else:
+            _arg(s, torch.float32, (M,), dev, "row scales")
     elif s is not None:
         raise ValueError("the mx format has no row scales")
-    _same_device(x, q=q, sf=sf, s=s)
-    _check(fn(_ptr(x), M, K, ld, code, _ptr(q), _rows(q, "q"), _ptr(sf), _ptr(s), _stream(stream)), name)
+    _check(fn(x.data_ptr(), M, K, ld, code, q.data_ptr(), ldq, sf.data_ptr(), _ptr(s), _stream(stream)), name)
     return q, sf, s
 
 
@@ -747,35 +777,31 @@ def dq_fp4_tile_scales(scales: torch.Tensor, fmt="nv", sf: torch.Tensor = None, 
     """Block scale bytes uint8 [rows, K/block] (ue8m0 for "mx", e4m3 for "nv")
     -> the tiled layout the kernels read."""
     code = _fp4_fmt(fmt)
+    dev = _here(scales, "scales")
     _need(scales, torch.uint8, "scales", 2)
     _contig(scales, "scales")
     R, G = scales.shape
     K = G * (16 if code == DQ_FP4_NV else 32)
+    if K < 1 or K % 32 != 0:
+        raise ValueError("scales: a row must hold the scales of a positive multiple of 32 features")
     shape = _fp4_scale_shape(R, K, code)
     if sf is None:
-        sf = torch.empty(shape, dtype=torch.uint8, device=scales.device)
-    _need(sf, torch.uint8, "sf", 3)
-    _contig(sf, "sf")
-    if tuple(sf.shape) != shape:
-        raise ValueError(f"sf must be {shape}")
-    _same_device(scales, sf=sf)
+        sf = scales.new_empty(shape)
+    _arg(sf, torch.uint8, shape, dev, "sf")
     _check(lib.dq_fp4_tile_scales(_ptr(scales), R, K, code, _ptr(sf), _stream(stream)), "dq_fp4_tile_scales")
     return sf
 
 
-def _fp4_operand(q, sf, s, code, name):
-    _need(q, torch.uint8, name, 2)
-    _contig(q, name)
-    R, K = q.shape[0], q.shape[1] * 2
-    _need(sf, torch.uint8, f"{name} scales", 3)
-    _contig(sf, f"{name} scales")
-    if tuple(sf.shape) != _fp4_scale_shape(R, K, code):
-        raise ValueError(f"{name} scales: expected {_fp4_scale_shape(R, K, code)}, got {tuple(sf.shape)}")
+def _fp4_operand(q, sf, s, code: int, dev: int, name: str):
+    """(rows, K) of a 4-bit operand with its tiled block scales and row scales."""
+    if q.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dims, got {q.dim()}")
+    _arg(q, torch.uint8, q.shape, dev, name)
+    R, K = q.shape
+    K *= 2
+    _arg(sf, torch.uint8, _fp4_scale_shape(R, K, code), dev, f"{name} scales")
     if s is not None:
-        _need(s, torch.float32, f"{name} row scales", 1)
-        _contig(s, f"{name} row scales")
-        if s.numel() != R:
-            raise ValueError(f"{name} row scales: expected {R}, got {s.numel()}")
+        _arg(s, torch.float32, (R,), dev, f"{name} row scales")
     return R, K
 
 
@@ -783,17 +809,23 @@ def dq_fp4_dequantize(q, sf, s=None, fmt="nv", out=None, stream=None) -> torch.T
     """The values 4-bit codes stand for: bf16 [rows, K] = e2m1 * block scale * s
     (s fp32 [rows] or None)."""
     code = _fp4_fmt(fmt)
-    M, K = _fp4_operand(q, sf, s, code, "q")
+    dev = _here(q, "q")
+    M, K = _fp4_operand(q, sf, s, code, dev, "q")
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, "out", 2)
-    _contig(out, "out")
-    if tuple(out.shape) != (M, K):
-        raise ValueError(f"out must be {(M, K)}")
-    _same_device(q, sf=sf, s=s, out=out)
-    _check(lib.dq_fp4_dequantize(_ptr(q), _ptr(sf), _ptr(s), M, K, code, _ptr(out), _stream(stream)),
+        out = q.new_empty((M, K), dtype=torch.bfloat16)
+    else:
+        _arg(out, torch.bfloat16, (M, K), dev, "out")
+    _check(lib.dq_fp4_dequantize(q.data_ptr(), sf.data_ptr(), _ptr(s), M, K, code, out.data_ptr(), _stream(stream)),
            "dq_fp4_dequantize")
     return out
+
+
+def _f32_or_bf16(out_dtype):
+    if out_dtype in ("bf16", torch.bfloat16):
+        return DQ_OUT_BF16, torch.bfloat16
+    if out_dtype in ("f32", "float32", torch.float32):
+        return DQ_OUT_F32, torch.float32
+    raise ValueError(f"out_dtype {out_dtype!r}")
 
 
 def dq_fp4_linear(A, sfa, s_row, W, sfw, s_col, bias=None, fmt="nv", out=None, out_dtype="bf16", stream=None):
@@ -802,49 +834,34 @@ def dq_fp4_linear(A, sfa, s_row, W, sfw, s_col, bias=None, fmt="nv", out=None, o
     block-scaled product on the tensor cores (or acc itself with
     out_dtype="f32").  s_row / s_col may be None (1)."""
     code = _fp4_fmt(fmt)
-    if out_dtype in ("f32", "float32", torch.float32, DQ_OUT_F32):
-        oc, odt = DQ_OUT_F32, torch.float32
-    elif out_dtype in ("bf16", torch.bfloat16, DQ_OUT_BF16):
-        oc, odt = DQ_OUT_BF16, torch.bfloat16
-    else:
-        raise ValueError(f"out_dtype {out_dtype!r}")
-    M, K = _fp4_operand(A, sfa, s_row, code, "A")
-    N, KW = _fp4_operand(W, sfw, s_col, code, "W")
+    oc, odt = _f32_or_bf16(out_dtype)
+    dev = _here(A, "A")
+    M, K = _fp4_operand(A, sfa, s_row, code, dev, "A")
+    N, KW = _fp4_operand(W, sfw, s_col, code, dev, "W")
     if K != KW:
         raise ValueError("A and W disagree on K")
     if bias is not None:
-        _need(bias, torch.bfloat16, "bias", 1)
-        _contig(bias, "bias")
-        if bias.numel() != N:
-            raise ValueError("bias length mismatch")
+        _arg(bias, torch.bfloat16, (N,), dev, "bias")
     if out is None:
-        out = torch.empty((M, N), dtype=odt, device=A.device)
-    _need(out, odt, "out", 2)
-    _contig(out, "out")
-    if tuple(out.shape) != (M, N):
-        raise ValueError(f"out: expected shape {(M, N)}, got {tuple(out.shape)}")
-    _same_device(A, sfa=sfa, s_row=s_row, W=W, sfw=sfw, s_col=s_col, bias=bias, out=out)
-    _check(lib.dq_fp4_linear(_ptr(A), _ptr(sfa), _ptr(s_row), M, K, _ptr(W), _ptr(sfw), _ptr(s_col), N, code,
-                             _ptr(bias), _ptr(out), oc, _stream(stream)), "dq_fp4_linear")
+        out = A.new_empty((M, N), dtype=odt)
+    else:
+        _arg(out, odt, (M, N), dev, "out")
+    _check(lib.dq_fp4_linear(A.data_ptr(), sfa.data_ptr(), _ptr(s_row), M, K, W.data_ptr(), sfw.data_ptr(),
+                             _ptr(s_col), N, code, _ptr(bias), out.data_ptr(), oc, _stream(stream)),
+           "dq_fp4_linear")
     return out
 
 
 # ---------------------------------------------------------------- 8-bit checkpoints
 
-def _act8_shapes(M: int, K: int):
-    g = (M + 31) // 32
-    return (2 * g, K, 16), (g, K)
-
-
-def _act8_operand(codes, scales, M: int):
-    _need(codes, torch.int8, "codes", 3)
-    _need(scales, torch.uint8, "scales", 2)
-    _contig(codes, "codes")
-    _contig(scales, "scales")
+def _act8_operand(codes, scales, M: int, dev: int) -> int:
+    """The feature count of the checkpoint of M tokens."""
+    if not isinstance(scales, torch.Tensor) or scales.dim() != 2:
+        raise ValueError("scales: expected a tensor of 2 dims")
     K = scales.shape[1]
-    want = _act8_shapes(M, K)
-    if tuple(codes.shape) != want[0] or tuple(scales.shape) != want[1]:
-        raise ValueError(f"{M} tokens of {K} features need codes {want[0]} and scales {want[1]}")
+    g = (M + 31) // 32
+    _arg(scales, torch.uint8, (g, K), dev, "scales")
+    _arg(codes, torch.int8, (2 * g, K, 16), dev, "codes")
     return K
 
 
@@ -852,34 +869,34 @@ def dq_act8_pack(x: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tens
     """An activation kept in 8 bits: x bf16 [M, K] (K % 16 == 0) -> (codes int8
     [2 ceil(M/32), K, 16], scales uint8 [ceil(M/32), K]); blocks of 32 tokens
     of one feature share a power-of-two scale."""
-    _need(x, torch.bfloat16, "x", 2)
-    ld = _rows(x, "x")
-    M, K = x.shape
+    dev = _here(x, "x")
+    M, K, ld = _rows(x, torch.bfloat16, "x")
     if K < 1 or K % 16 != 0:
         raise ValueError(f"x: the row length must be a positive multiple of 16, got {K}")
-    cs, ss = _act8_shapes(M, K)
+    g = (M + 31) // 32
     if codes is None:
-        codes = torch.empty(cs, dtype=torch.int8, device=x.device)
+        codes = x.new_empty((2 * g, K, 16), dtype=torch.int8)
+    else:
+        _arg(codes, torch.int8, (2 * g, K, 16), dev, "codes")
     if scales is None:
-        scales = torch.empty(ss, dtype=torch.uint8, device=x.device)
-    if _act8_operand(codes, scales, M) != K:
-        raise ValueError("codes and scales do not match x")
-    _same_device(x, codes=codes, scales=scales)
-    _check(lib.dq_act8_pack(_ptr(x), M, K, ld, _ptr(codes), _ptr(scales), _stream(stream)), "dq_act8_pack")
+        scales = x.new_empty((g, K), dtype=torch.uint8)
+    else:
+        _arg(scales, torch.uint8, (g, K), dev, "scales")
+    _check(lib.dq_act8_pack(x.data_ptr(), M, K, ld, codes.data_ptr(), scales.data_ptr(), _stream(stream)),
+           "dq_act8_pack")
     return codes, scales
 
 
 def dq_act8_unpack(codes, scales, M: int, out=None, stream=None) -> torch.Tensor:
     """The bf16 [M, K] values of an 8-bit checkpoint (exact)."""
-    K = _act8_operand(codes, scales, M)
+    dev = _here(codes, "codes")
+    K = _act8_operand(codes, scales, M, dev)
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
-    _need(out, torch.bfloat16, "out", 2)
-    _contig(out, "out")
-    if tuple(out.shape) != (M, K):
-        raise ValueError(f"out must be {(M, K)}")
-    _same_device(codes, scales=scales, out=out)
-    _check(lib.dq_act8_unpack(_ptr(codes), _ptr(scales), M, K, _ptr(out), _stream(stream)), "dq_act8_unpack")
+        out = codes.new_empty((M, K), dtype=torch.bfloat16)
+    else:
+        _arg(out, torch.bfloat16, (M, K), dev, "out")
+    _check(lib.dq_act8_unpack(codes.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(), _stream(stream)),
+           "dq_act8_unpack")
     return out
 
 
@@ -891,38 +908,26 @@ def dq_act8_weight_grad(dy, codes, scales, out=None, out_dtype="bf16", accumulat
     is None), True, or the fp32 tensor to fill.  With accumulate=True (fp32
     `out` given, and `bias_grad` a tensor or False) both are added to what the
     tensors hold."""
-    if out_dtype in ("f32", "float32", torch.float32, DQ_OUT_F32):
-        oc, odt = DQ_OUT_F32, torch.float32
-    elif out_dtype in ("bf16", torch.bfloat16, DQ_OUT_BF16):
-        oc, odt = DQ_OUT_BF16, torch.bfloat16
-    else:
-        raise ValueError(f"out_dtype {out_dtype!r}")
-    _need(dy, torch.bfloat16, "dy", 2)
-    ld = _rows(dy, "dy")
-    M, N = dy.shape
-    K = _act8_operand(codes, scales, M)
+    oc, odt = _f32_or_bf16(out_dtype)
+    dev = _here(dy, "dy")
+    M, N, ld = _rows(dy, torch.bfloat16, "dy")
+    K = _act8_operand(codes, scales, M, dev)
     if accumulate and (out is None or oc != DQ_OUT_F32 or bias_grad is True):
         raise ValueError("accumulate needs the fp32 tensors to add to")
     if out is None:
-        out = torch.empty((N, K), dtype=odt, device=dy.device)
-    _need(out, odt, "out", 2)
-    _contig(out, "out")
-    if tuple(out.shape) != (N, K):
-        raise ValueError(f"out must be {(N, K)}")
+        out = dy.new_empty((N, K), dtype=odt)
+    else:
+        _arg(out, odt, (N, K), dev, "out")
     db = None
     if bias_grad is True:
-        db = torch.empty((N,), dtype=torch.float32, device=dy.device)
+        db = dy.new_empty((N,), dtype=torch.float32)
     elif bias_grad is not False and bias_grad is not None:
         db = bias_grad
-        _need(db, torch.float32, "bias_grad", 1)
-        _contig(db, "bias_grad")
-        if db.numel() != N:
-            raise ValueError("bias_grad length mismatch")
-    _same_device(dy, codes=codes, scales=scales, out=out, bias_grad=db)
+        _arg(db, torch.float32, (N,), dev, "bias_grad")
     if M <= 1:                        # a single row has no stride to speak of
         ld = (ld + 7) // 8 * 8
-    _check(lib.dq_act8_weight_grad(_ptr(dy), M, N, ld, _ptr(codes), _ptr(scales), K, _ptr(out), oc, int(accumulate),
-                                   _ptr(db), _stream(stream)), "dq_act8_weight_grad")
+    _check(lib.dq_act8_weight_grad(dy.data_ptr(), M, N, ld, codes.data_ptr(), scales.data_ptr(), K, out.data_ptr(),
+                                   oc, int(accumulate), _ptr(db), _stream(stream)), "dq_act8_weight_grad")
     return out, db
 
 
