@@ -98,15 +98,34 @@ __device__ __forceinline__ uint32_t e2m1_by_borders(float ax, float d, bool neg)
 }
 
 // ---------------------------------------------------------------- bf16 rows
-// Register-resident: 2^tpr_log2 (32..256) threads own a row, up to VPT
-// 16-byte vectors (8 features) each.  An NV block is 2 lanes, an MX block 4.
-// For NV codes the quotient is x * c with c = 1 / (s d) rounded: within 2^-23
-// of x / (s d).  X = x / s has 8 significant bits and border * d at most 7, so
-// the exact quotient either equals a border or is at least 2^-10 away from it
-// (2^-8 relative, the least border being 1/4); rounding the product to a
-// multiple of 2^-10 (one addition and subtraction of 1.5 * 2^13) therefore
-// restores ties exactly and moves nothing across a border.
-template <bool NV, int VPT>
+__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p)), b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+
+// Register-resident: 2^tpr_log2 (32..256) threads own a row, up to VPT runs of
+// 16 features (32 bytes, one load) each: an NV block is one run, an MX block
+// two neighbouring lanes'.
+//
+// For NV, two roundings are decided without a division, both because bf16 has
+// 8 significant bits.  (1) The e4m3 scale of t / 6, t = a / s exact: a rounding
+// border B of e4m3 has 5 significant bits and 6 B at most 7, so t / 6 is either
+// exactly a border or at least 2^-8 (relative) away from it; t * fp32(1/6) is
+// within 2^-23 of t / 6, so rounding it to 12 significant bits restores the
+// borders exactly and moves nothing across one.  (2) The code of x / (s d):
+// the product with c = 1 / (s d) (approximate reciprocal) is within 2^-22 of
+// the quotient X / d, X = x / s; border * d has at most 7 significant bits, so
+// X / d is a border or at least 2^-10 away from it (2^-8 relative, the least
+// border being 1/4), and rounding to a multiple of 2^-10 (adding and
+// subtracting 1.5 * 2^13) again restores ties and crosses nothing.
+template <bool NV, int VPT, bool WIDE>
 __global__ void __launch_bounds__(256) fp4_rows_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                        int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
                                                        uint8_t* __restrict__ sf, int64_t sf_atoms,
@@ -117,28 +136,29 @@ __global__ void __launch_bounds__(256) fp4_rows_kernel(const uint16_t* __restric
   const int t = threadIdx.x & (tpr - 1);
   const int r_local = threadIdx.x >> tpr_log2;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 >> tpr_log2) + r_local;
-  const int nv = static_cast<int>(K / 8);
+  const int nu = static_cast<int>(K / 16);
   const bool in = row < M;               // rows up to the next multiple of 128 get zero scales
   __shared__ uint32_t warp_max[8];
 
-  uint4 v[VPT];
-  const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
+  uint32_t v[VPT][8];
+  const uint16_t* xr = x + row * ldx;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vi = t + i * tpr;
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && vi < nv) v[i] = __ldcs(xr + vi);
+    const int u = t + i * tpr;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0u;
+    if (in && u < nu) load16(v[i], xr + u * 16, WIDE);
   }
   // magnitudes order like their bits, NaN above infinity above the rest
   uint32_t top[VPT];
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const uint32_t m = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
-                                __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+    uint32_t m = v[i][0] & 0x7fff7fffu;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = __vmaxu2(m, v[i][j] & 0x7fff7fffu);
     uint32_t b = max(m & 0xffffu, m >> 16);
-    b = max(b, __shfl_xor_sync(0xffffffffu, b, 1));
-    if (!NV) b = max(b, __shfl_xor_sync(0xffffffffu, b, 2));
+    if (!NV) b = max(b, __shfl_xor_sync(0xffffffffu, b, 1));
     top[i] = b << 16;                    // fp32 bits
     amax = max(amax, top[i]);
   }
@@ -163,39 +183,43 @@ __global__ void __launch_bounds__(256) fp4_rows_kernel(const uint16_t* __restric
   uint8_t* qr = q + row * ldq;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int vi = t + i * tpr;
+    const int u = t + i * tpr;
     uint32_t byte;
     float c;
     bool zero;
     if constexpr (NV) {
-      byte = e4m3_byte(__fdiv_rn(__uint_as_float(top[i]) * inv_s, 6.0f));
-      if (bad_row) byte = 0;
+      const uint32_t r = __float_as_uint(__uint_as_float(top[i]) * inv_s * (1.0f / 6.0f));
+      byte = bad_row ? 0u : e4m3_byte(__uint_as_float((r + 0x800u) & 0xfffff000u));
       zero = byte == 0;
-      c = zero ? 0.0f : __fdiv_rn(1.0f, e4m3_value(byte)) * inv_s;
+      float rcp;
+      asm("rcp.approx.f32 %0, %1;" : "=f"(rcp) : "f"(e4m3_value(byte)));
+      c = zero ? 0.0f : rcp * inv_s;
     } else {
       byte = mx_scale(top[i], c);
       zero = byte == 255u;
     }
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    float y[8];
+    const uint64_t c2 = pack_f2(c, c), up = pack_f2(12288.0f, 12288.0f), down = pack_f2(-12288.0f, -12288.0f);
+    uint32_t codes[2];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      y[2 * h] = __uint_as_float(w[h] << 16) * c;
-      y[2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u) * c;
-      if constexpr (NV) {
-        y[2 * h] = __fsub_rn(__fadd_rn(y[2 * h], 12288.0f), 12288.0f);
-        y[2 * h + 1] = __fsub_rn(__fadd_rn(y[2 * h + 1], 12288.0f), 12288.0f);
+    for (int h = 0; h < 2; ++h) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = v[i][4 * h + j];
+        uint64_t p = mul_f2(pack_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), c2);
+        if constexpr (NV) p = add_f2(add_f2(p, up), down);
+        unpack_f2(p, y[2 * j], y[2 * j + 1]);
       }
+      codes[h] = zero ? 0u : e2m1x8(y);
     }
-    const uint32_t codes = zero ? 0u : e2m1x8(y);
-    // four neighbouring blocks' scale bytes as one word
-    uint32_t word = vi < nv ? byte << (8 * ((vi >> (NV ? 1 : 2)) & 3)) : 0u;
+    // four neighbouring blocks' scale bytes as one word (an MX block's two lanes hold the same byte)
+    uint32_t word = u < nu ? byte << (8 * ((NV ? u : u >> 1) & 3)) : 0u;
+    word |= __shfl_xor_sync(0xffffffffu, word, NV ? 1 : 2);
     word |= __shfl_xor_sync(0xffffffffu, word, NV ? 2 : 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, NV ? 4 : 8);
-    if (vi < nv) {
-      if (in) *reinterpret_cast<uint32_t*>(qr + static_cast<int64_t>(vi) * 4) = codes;
-      if ((vi & (NV ? 7 : 15)) == 0)
-        *reinterpret_cast<uint32_t*>(sf + srow_off + static_cast<int64_t>(vi >> (NV ? 3 : 4)) * 512) = in ? word : 0u;
+    if (u < nu) {
+      if (in) *reinterpret_cast<uint2*>(qr + static_cast<int64_t>(u) * 8) = make_uint2(codes[0], codes[1]);
+      if ((u & (NV ? 3 : 7)) == 0)
+        *reinterpret_cast<uint32_t*>(sf + srow_off + static_cast<int64_t>(u >> (NV ? 2 : 3)) * 512) = in ? word : 0u;
     }
   }
 }
@@ -357,17 +381,18 @@ dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, in
   const int64_t rows = (M + 127) / 128 * 128;
   const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
   if constexpr (sizeof(T) == 2) {
-    if (K <= 16384 && ldx % 8 == 0 && aligned(x, 16) && ldq % 4 == 0 && aligned(q, 4)) {
-      // 4 vectors per thread where 256 threads hold the row so, else 8
-      const int64_t nv = K / 8;
-      int vpt = nv <= 32 ? 1 : nv <= 64 ? 2 : 4;
+    if (K <= 16384 && ldx % 8 == 0 && aligned(x, 16) && ldq % 8 == 0 && aligned(q, 8)) {
+      // two runs per thread where 256 threads hold the row so, else four
+      const int64_t nu = K / 16;
+      int vpt = nu <= 32 ? 1 : 2;
       int lg = 5;
-      while (lg < 8 && (static_cast<int64_t>(vpt) << lg) < nv) ++lg;
-      if ((static_cast<int64_t>(vpt) << lg) < nv) vpt = 8;
+      while (lg < 8 && (static_cast<int64_t>(vpt) << lg) < nu) ++lg;
+      if ((static_cast<int64_t>(vpt) << lg) < nu) vpt = 4;
       const int64_t blocks = (rows + (256 >> lg) - 1) / (256 >> lg);
-      if (blocks > 0x7fffffff) return DQ_ERR_UNSUPPORTED;
-      auto k = vpt == 1 ? fp4_rows_kernel<NV, 1> : vpt == 2 ? fp4_rows_kernel<NV, 2>
-               : vpt == 4 ? fp4_rows_kernel<NV, 4> : fp4_rows_kernel<NV, 8>;
+      const bool wide = aligned(x, 32) && ldx % 16 == 0;
+      auto k = vpt == 1   ? (wide ? fp4_rows_kernel<NV, 1, true> : fp4_rows_kernel<NV, 1, false>)
+               : vpt == 2 ? (wide ? fp4_rows_kernel<NV, 2, true> : fp4_rows_kernel<NV, 2, false>)
+                          : (wide ? fp4_rows_kernel<NV, 4, true> : fp4_rows_kernel<NV, 4, false>);
       return launch(k, blocks, stream, x, M, K, ldx, q, ldq, sf, atoms, s_row, lg);
     }
   }
