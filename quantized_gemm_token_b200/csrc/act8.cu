@@ -73,17 +73,18 @@ __global__ void __launch_bounds__(128) act8_pack_kernel(const uint16_t* __restri
     // subnormals, whose block scale is 2^-127 like the least normal's)
     const uint32_t top[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
     uint32_t e[4];
-    float up[4];                           // 2^(133 - E), as two factors where it overflows
-    float up2[4];
+    uint64_t up[4], up2[4];                // 2^(133 - E) twice, as two factors (one would overflow for E < 6)
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       e[f] = top[f] >> 7;
-      const bool bad = e[f] >= 255u;
       const int s = 133 - static_cast<int>(e[f]);       // -122 .. 133
       const int s1 = s > 127 ? 127 : s;
-      up[f] = bad ? 0.0f : __uint_as_float(static_cast<uint32_t>(s1 + 127) << 23);
-      up2[f] = __uint_as_float(static_cast<uint32_t>(s - s1 + 127) << 23);
+      const float u1 = e[f] >= 255u ? 0.0f : __uint_as_float(static_cast<uint32_t>(s1 + 127) << 23);
+      const float u2 = __uint_as_float(static_cast<uint32_t>(s - s1 + 127) << 23);
+      up[f] = pack_f2(u1, u1);
+      up2[f] = pack_f2(u2, u2);
     }
+    const uint64_t magic = pack_f2(12582912.0f, 12582912.0f);
     *reinterpret_cast<uint32_t*>(scales + blk * K + k) = e[0] | (e[1] << 8) | (e[2] << 16) | (e[3] << 24);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -93,19 +94,20 @@ __global__ void __launch_bounds__(128) act8_pack_kernel(const uint16_t* __restri
         uint32_t w[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          uint32_t b[4];
+          uint32_t c[2];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint2 c = v[16 * h + 4 * g + u];
-            const uint32_t bits = (f < 2 ? c.x : c.y);
-            const float xv = __uint_as_float((f & 1) ? bits & 0xffff0000u : bits << 16);
-            float y = __fmul_rn(__fmul_rn(xv, up[f]), up2[f]);       // exact
-            y = fminf(fmaxf(y, -127.0f), 127.0f);
-            b[u] = __float_as_uint(__fadd_rn(y, 12582912.0f));       // low byte = rint(y)
+          for (int u = 0; u < 2; ++u) {    // tokens 2u, 2u + 1 of the four
+            const uint2 v0 = v[16 * h + 4 * g + 2 * u], v1 = v[16 * h + 4 * g + 2 * u + 1];
+            const uint32_t b0 = f < 2 ? v0.x : v0.y, b1 = f < 2 ? v1.x : v1.y;
+            const uint64_t x2 = (f & 1) ? pack_f2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))
+                                        : pack_f2(__uint_as_float(b0 << 16), __uint_as_float(b1 << 16));
+            // the scaling is exact; adding 1.5 * 2^23 leaves rint(y), -128 .. 128, in the low 16 bits
+            const uint64_t t = add_f2(mul_f2(mul_f2(x2, up[f]), up2[f]), magic);
+            const uint32_t r = __byte_perm(static_cast<uint32_t>(t), static_cast<uint32_t>(t >> 32), 0x5410);
+            c[u] = __vmaxs2(__vmins2(r, 0x007f007fu), 0xff81ff81u);
           }
-          w[g] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+          w[g] = e[f] >= 255u ? 0u : __byte_perm(c[0], c[1], 0x6420);
         }
-        if (e[f] >= 255u) w[0] = w[1] = w[2] = w[3] = 0u;
         dst[f] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }

@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(256) fp4_generic_kernel(const T* __restrict__ 
 
 // ---------------------------------------------------------------- dequantize
 // One thread per 16 codes: w = bf16((e2m1 * d) * s), the block product exact.
-template <bool NV>
+// WIDE: a 32-byte aligned output, one store per thread.
+template <bool NV, bool WIDE>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
                                                           const float* __restrict__ s_row, int64_t M, int64_t K,
                                                           int64_t sf_atoms, uint16_t* __restrict__ out) {
@@ -336,9 +337,15 @@ __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restr
           : "r"(h2));
       asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[h]) : "f"(__fmul_rn(__fmul_rn(hi, d), s)), "f"(__fmul_rn(__fmul_rn(lo, d), s)));
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + i * 16);
-    __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-    __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    uint16_t* dst = out + i * 16;
+    if (WIDE) {
+      asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]),
+                   "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                   : "memory");
+    } else {
+      __stcs(reinterpret_cast<uint4*>(dst), make_uint4(o[0], o[1], o[2], o[3]));
+      __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    }
   }
 }
 
@@ -452,8 +459,10 @@ dq_status dq_fp4_dequantize(const uint8_t* q, const uint8_t* sf, const float* s,
   const int64_t want = (M * (K / 16) + 255) / 256;
   const int64_t blocks = want < kMaxGrid ? want : kMaxGrid;
   auto cs = reinterpret_cast<cudaStream_t>(stream);
-  return launch(fmt == DQ_FP4_NV ? fp4_dequant_kernel<true> : fp4_dequant_kernel<false>, blocks, cs, q, sf, s, M, K,
-                fp4_atoms(K, fmt), static_cast<uint16_t*>(out_bf16));
+  const bool wide = aligned(out_bf16, 32);
+  auto k = fmt == DQ_FP4_NV ? (wide ? fp4_dequant_kernel<true, true> : fp4_dequant_kernel<true, false>)
+                            : (wide ? fp4_dequant_kernel<false, true> : fp4_dequant_kernel<false, false>);
+  return launch(k, blocks, cs, q, sf, s, M, K, fp4_atoms(K, fmt), static_cast<uint16_t*>(out_bf16));
 }
 
 dq_status dq_fp4_tile_scales(const uint8_t* scales, int64_t rows, int64_t K, int fmt, uint8_t* sf, dq_stream_t stream) {
