@@ -14,21 +14,27 @@
 //    memory saves its write and the tensor core's read (2 x 16 KB per 64
 //    tokens x 128 features), the bound of the kernels here that build an
 //    operand in shared memory.
-// Roles (five warpgroups): warp 0 dY producer, warp 1 MMA issuer, warp 2 code
-// producer; two warpgroups of converters taking alternate 64-token steps; two
-// warpgroups of accumulating epilogue warps (lane = feature, a warp holds half
-// of the tile's channels in registers).
+// A pair of SMs (cta_group::2) per tile of 256 features x 256 (or 128)
+// channels: each CTA converts its own 128 features into its own tensor memory
+// and loads half of the channels, which the pair's tensor cores share.  Alone,
+// a CTA loads 41 KB per 64-token step, 640 cycles at the 64 bytes per cycle an
+// SM takes from L2, against 512 cycles of MMAs; in a pair 25 KB.
+// Roles (five warpgroups per CTA): warp 0 dY producer, warp 1 MMA issuer (rank
+// 0 only), warp 2 code producer; two warpgroups of converters taking
+// alternate 64-token steps; two warpgroups of accumulating epilogue warps
+// (lane = feature, a warp holds half of the tile's channels in registers).
 // Three rings, each as deep as its own round trip asks: dY in shared memory
 // (freed by the MMAs), codes in shared memory (freed by the converters), and
-// converted steps in tensor memory.  With one ring for both loads a step's
-// slot waited for copy, conversion AND product in turn (0.34 us per step with
-// neither arithmetic nor MMAs in it).
+// converted steps in tensor memory.
 // Sums: the tensor core truncates when it adds to its accumulator, so a chain
 // of MMAs loses about 2^-26 of the sum per instruction, all in one direction
 // (65792 tokens in one chain: 4.4e-5 of the result).  Every 1024 tokens the
 // epilogue adds the accumulator to fp32 registers (rounding to nearest) and
-// the chain starts anew; the eight converted steps in flight cover the read.
-// Few tiles: the tokens are split over a cluster of up to 8 CTAs whose fp32
+// the chain starts anew; the converted steps in flight cover the read.
+// db: in the tiles of the first 256 features the epilogue warps also add up
+// the dY tile that lies in shared memory (each lane eight channels), so dY is
+// not read again: there a stage's MMAs hand it to them, and they free it.
+// Few tiles: the tokens are split over a cluster of up to 4 pairs whose fp32
 // partial tiles are added through distributed shared memory in split order
 // (no workspace, no atomics).
 #include <cuda_bf16.h>
@@ -55,7 +61,7 @@ constexpr int WG_REGS_ISSUE = 40, WG_REGS_CVT = 56, WG_REGS_EPI = 160;
 constexpr int WG_STEP = 64;                  // tokens per step
 constexpr int WG_SEG = 16;                   // steps per accumulator chain
 constexpr int WG_CODES = 128 * WG_STEP;      // bytes: [4 x 16 tokens][128 features][16]
-constexpr int WG_MAX_RING = 8;               // stages or slots of each ring
+constexpr int WG_RING = 8;                   // stages or slots of each ring
 constexpr int WG_CODE_STAGE = WG_CODES + 256;
 constexpr int WG_BAR_BYTES = 512;
 constexpr int WG_OUT_BUF = 2048;             // per epilogue warp: 32 x 32 bf16 or 16 x 32 fp32
@@ -64,30 +70,29 @@ constexpr int64_t kGradMaxDim = int64_t(1) << 30;
 
 struct GradArgs {
   int M, N, K;
-  int bn;                  // channels per tile (64, 128, 192 or 256)
-  int kt, nt;              // feature tiles (128), channel tiles
+  int bn;                  // channels per tile (128 or 256), half of them per CTA
+  int kt, nt;              // feature tiles (256), channel tiles
   int splits, units;
   int ks;                  // token steps: ceil(M / 64)
-  int stages, code_stages; // dY and code rings
-  int slots;               // converted-step slots in tensor memory, after the accumulator
   int full_chunks;         // N / 64: chunks the 3-D map covers
   uint32_t off_q, off_out, off_bar;
   void* dw;
+  float* db;               // or null
   int f32, accumulate;
   WaitCtl wait;
 };
 
 // kind::f16, bf16 A (tensor memory, K-major) and B (shared memory, MN-major),
-// fp32 accumulator.
+// fp32 accumulator, M = 256 over the pair.
 __host__ __device__ constexpr uint32_t idesc_grad(int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (16u << 24);
 }
 
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -100,9 +105,29 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t chunk) 
          (static_cast<uint64_t>(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
+// Arrive once on the mbarrier at shared::cta offset `bar` in both CTAs of the
+// pair (`mask`: their bits in the cluster) when all MMAs issued so far by this
+// thread have completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   bar),
+               "h"(mask)
+               : "memory");
+}
+
+// Arrive on the mbarrier at shared::cluster address `bar` for tensor-memory
+// writes (waited for, and fenced by tcgen05.fence::before_thread_sync): they
+// are not ordered by the arrive itself, so it needs no release (which at
+// cluster scope takes more than the 512 cycles of a step).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 3-D tiled load into this CTA's shared memory, completing on the pair
+// leader's mbarrier.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
@@ -183,15 +208,17 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw);
-  // rings: dY (bn / 64 chunks of 64 tokens x 128 B); codes, then their scales [2][128]
-  const uint32_t y_bytes = static_cast<uint32_t>(g.bn) * 128u;
-  uint64_t* const yfull = reinterpret_cast<uint64_t*>(smem + g.off_bar);
-  uint64_t* const yempty = yfull + WG_MAX_RING;
-  uint64_t* const qfull = yempty + WG_MAX_RING;
-  uint64_t* const qempty = qfull + WG_MAX_RING;
-  uint64_t* const afull = qempty + WG_MAX_RING;    // a slot holds a converted step
-  uint64_t* const aempty = afull + WG_MAX_RING;
-  uint64_t* const accf = aempty + WG_MAX_RING;
+  // rings: this CTA's half of dY (bn / 128 chunks of 64 tokens x 128 B); codes, then their scales [2][128]
+  const int half_n = g.bn / 2;
+  const uint32_t y_bytes = static_cast<uint32_t>(half_n) * 128u;
+  uint64_t* const yfull = reinterpret_cast<uint64_t*>(smem + g.off_bar);   // leader: both halves of dY
+  uint64_t* const yempty = yfull + WG_RING;
+  uint64_t* const qfull = yempty + WG_RING;
+  uint64_t* const qempty = qfull + WG_RING;
+  uint64_t* const afull = qempty + WG_RING;        // leader: both CTAs' slots hold a converted step
+  uint64_t* const aempty = afull + WG_RING;
+  uint64_t* const ydone = aempty + WG_RING;        // the MMAs are done with a stage that column sums still read
+  uint64_t* const accf = ydone + WG_RING;
   uint64_t* const acce = accf + 1;
   uint64_t* const drain = acce + 1;
   uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -199,18 +226,25 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1u;                // in the pair
+  const uint32_t lead = crank & ~1u;               // the pair's leader in the cluster
+  const uint16_t mask = static_cast<uint16_t>(3u << lead);
+  const int G = static_cast<int>(gridDim.x) >> 1;
+  const int u0 = static_cast<int>(blockIdx.x) >> 1;
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < WG_MAX_RING; ++i) {
+    for (int i = 0; i < WG_RING; ++i) {
       mbar_init(smem_u32(yfull + i), 1);
       mbar_init(smem_u32(yempty + i), 1);
       mbar_init(smem_u32(qfull + i), 1);
       mbar_init(smem_u32(qempty + i), 4);
-      mbar_init(smem_u32(afull + i), 4);
+      mbar_init(smem_u32(afull + i), 8);
       mbar_init(smem_u32(aempty + i), 1);
+      mbar_init(smem_u32(ydone + i), 1);
     }
     mbar_init(smem_u32(accf), 1);
-    mbar_init(smem_u32(acce), WG_EPI_WARPS);
+    mbar_init(smem_u32(acce), 2 * WG_EPI_WARPS);
     mbar_init(smem_u32(drain), 1);
     fence_barrier_init();
     tma_prefetch_desc(&tm_y3);
@@ -219,11 +253,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     tma_prefetch_desc(&tm_c);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_holder), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(tmem_holder), 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync_all();            // the barriers are initialised before any remote use
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   griddep_wait();
@@ -236,15 +270,15 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       const bool codes = warp == 2;
       uint64_t* const full = codes ? qfull : yfull;
       uint64_t* const empty = codes ? qempty : yempty;
-      const int ring = codes ? g.code_stages : g.stages;
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      const int chunks = g.bn / 64;
-      for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      const int chunks = half_n / 64;
+      for (int u = u0; ok && u < g.units; u += G) {
         const GradUnit t = grad_unit(g, u);
-        const int c0 = t.nt * chunks;
+        const int c0 = t.nt * 2 * chunks + static_cast<int>(rank) * chunks;
+        const int f0 = t.kt * 256 + static_cast<int>(rank) * 128;
         // the 3-D map covers whole chunks only: a tile that holds the ragged last one is loaded chunk by chunk
         const bool whole = c0 + chunks <= g.full_chunks || g.N % 64 == 0;
         for (int s = t.s0; s < t.s1; ++s) {
@@ -258,37 +292,51 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
           if (elect_one()) {
             if (codes) {
               mbar_arrive_expect_tx(fb, WG_CODE_STAGE);
-              tma_load_2d(sq, &tm_q, fb, t.kt * 256, s * 4);
-              tma_load_2d(sq + WG_CODES, &tm_e, fb, t.kt * 128, s * 2);
+              tma_load_2d(sq, &tm_q, fb, f0 * 2, s * 4);
+              tma_load_2d(sq + WG_CODES, &tm_e, fb, f0, s * 2);
             } else {
-              mbar_arrive_expect_tx(fb, y_bytes);
+              if (rank == 0) mbar_arrive_expect_tx(fb, 2u * y_bytes);
+              const uint32_t fl = map_to_rank(fb, lead);
               if (whole)
-                tma_load_3d(sy, &tm_y3, fb, 0, s * WG_STEP, c0);
+                tma_load_3d_pair(sy, &tm_y3, fl, 0, s * WG_STEP, c0);
               else
                 for (int c = 0; c < chunks; ++c)
-                  tma_load_2d(sy + static_cast<uint32_t>(c) * 8192u, &tm_y2, fb, (c0 + c) * 64, s * WG_STEP);
+                  tma_load_2d_pair(sy + static_cast<uint32_t>(c) * 8192u, &tm_y2, fl, (c0 + c) * 64, s * WG_STEP);
             }
           }
           __syncwarp();
           ++issued;
-          if (++stage == ring) {
+          if (++stage == WG_RING) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
-      // every copy issued lands before the CTA can exit
+      // Every copy issued lands before the CTA can exit: the leader's barriers
+      // tell; rank 1, whose dY copies complete on the leader's, exits after the
+      // leader's MMAs (drain), and after a failed wait a while later.
       volatile int never = 0;
-      for (long long i = issued > ring ? issued - ring : 0; i < issued; ++i)
-        pipe::wait(smem_u32(full + static_cast<int>(i % ring)), static_cast<uint32_t>((i / ring) & 1), g.wait, &never);
-    } else if (warp == 1) {
+      if (codes || rank == 0) {
+        for (long long i = issued > WG_RING ? issued - WG_RING : 0; i < issued; ++i)
+          pipe::wait(smem_u32(full + static_cast<int>(i % WG_RING)), static_cast<uint32_t>((i / WG_RING) & 1), g.wait,
+                     &never);
+      } else {
+        pipe::wait(smem_u32(drain), 0, g.wait, &never);
+        if (!ok) {
+          const uint64_t w0 = globaltimer();
+          while (globaltimer() - w0 < 100000ull) {
+          }
+        }
+      }
+    } else if (warp == 1 && rank == 0) {
       // -------------------------------------------------------- MMA issuer
       const uint32_t idesc = idesc_grad(g.bn);
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, sphase = 0, aphase = 0;
+      int stage = 0;
+      uint32_t phase = 0, aphase = 0;
       bool ok = true, tested = false;             // tested: the next step's operands were found ready
-      for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+      for (int u = u0; ok && u < g.units; u += G) {
         const GradUnit t = grad_unit(g, u);
+        uint64_t* const ynext = g.db != nullptr && t.kt == 0 ? ydone : yempty;
         for (int s = t.s0; ok && s < t.s1;) {
           const int end = min(t.s1, s + WG_SEG);
           if (!mbar_wait_warp(smem_u32(acce), aphase ^ 1, g.wait, abort_flag)) {
@@ -298,40 +346,36 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
           aphase ^= 1;
           tc_fence_after();
           for (int first = s; s < end; ++s) {
-            if (!mbar_wait_warp2(tested, smem_u32(yfull + stage), phase, smem_u32(afull + slot), sphase, g.wait,
+            if (!mbar_wait_warp2(tested, smem_u32(yfull + stage), phase, smem_u32(afull + stage), phase, g.wait,
                                  abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
             const uint64_t bd = smem_desc_mn(base + static_cast<uint32_t>(stage) * y_bytes, 8192u);
-            const uint32_t a = tmem + static_cast<uint32_t>(g.bn + slot * WG_SLOT_COLS);
-            const uint32_t yb = smem_u32(yempty + stage), ab = smem_u32(aempty + slot);
-            if (++slot == g.slots) {
-              slot = 0;
-              sphase ^= 1;
-            }
-            if (++stage == g.stages) {
+            const uint32_t a = tmem + static_cast<uint32_t>(256 + stage * WG_SLOT_COLS);
+            const uint32_t yb = smem_u32(ynext + stage), ab = smem_u32(aempty + stage);
+            if (++stage == WG_RING) {
               stage = 0;
               phase ^= 1;
             }
-            const bool ty = mbar_test(smem_u32(yfull + stage), phase), ta = mbar_test(smem_u32(afull + slot), sphase);
+            const bool ty = mbar_test(smem_u32(yfull + stage), phase), ta = mbar_test(smem_u32(afull + stage), phase);
             if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)      // 16 tokens: 8 columns of A, 2048 bytes of B
-                mma_bf16_ts(tmem, a + 8 * j, bd + 128 * j, idesc, (s > first || j > 0) ? 1u : 0u);
-              mma_commit(yb);
-              mma_commit(ab);
+                mma_bf16_ts_pair(tmem, a + 8 * j, bd + 128 * j, idesc, (s > first || j > 0) ? 1u : 0u);
+              commit_pair(yb, mask);
+              commit_pair(ab, mask);
             }
             __syncwarp();
-            tested = ty && ta;
+            tested = __all_sync(0xffffffffu, ty && ta);
           }
           if (!ok) break;
-          if (elect_one()) mma_commit(smem_u32(accf));
+          if (elect_one()) commit_pair(smem_u32(accf), mask);
           __syncwarp();
         }
       }
-      if (elect_one()) mma_commit(smem_u32(drain));
+      if (elect_one()) commit_pair(smem_u32(drain), mask);
       __syncwarp();
       volatile int never = 0;
       pipe::wait(smem_u32(drain), 0, g.wait, &never);
@@ -342,29 +386,25 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     const int grp = (warp - WG_CVT_WARP0) >> 2;
     const int q = warp & 3;                      // TMEM sub-partition
     const uint32_t feat = static_cast<uint32_t>(q * 32 + lane);
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(g.bn);
-    int stage = 0, slot = 0;                     // ring positions of the CTA's current step, over its units
-    uint32_t phase = 0, sphase = 0;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16) + 256u;
+    int stage = 0;                               // ring position of the CTA's current step, over its units
+    uint32_t phase = 0;
     int turn = 0;
     bool ok = true;
     auto advance = [&]() {
       turn ^= 1;
-      if (++stage == g.code_stages) {
+      if (++stage == WG_RING) {
         stage = 0;
         phase ^= 1;
       }
-      if (++slot == g.slots) {
-        slot = 0;
-        sphase ^= 1;
-      }
     };
-    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+    for (int u = u0; ok && u < g.units; u += G) {
       const GradUnit t = grad_unit(g, u);
       for (int s = t.s0; s < t.s1; ++s, advance()) {
         if (turn != grp) continue;
         // the step's codes have landed, its slot's previous MMAs completed
-        const bool tq = mbar_test(smem_u32(qfull + stage), phase), ta = mbar_test(smem_u32(aempty + slot), sphase ^ 1);
-        if (!mbar_wait_warp2(tq && ta, smem_u32(qfull + stage), phase, smem_u32(aempty + slot), sphase ^ 1, g.wait,
+        const bool tq = mbar_test(smem_u32(qfull + stage), phase), ta = mbar_test(smem_u32(aempty + stage), phase ^ 1);
+        if (!mbar_wait_warp2(tq && ta, smem_u32(qfull + stage), phase, smem_u32(aempty + stage), phase ^ 1, g.wait,
                              abort_flag)) {
           ok = false;
           break;
@@ -386,14 +426,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             for (int i = 0; i < 8; ++i) codes4_top(cw[i], e, r[2 * i], r[2 * i + 1]);
           }
           __syncwarp();
-          tmem_st_32x32b_x16(lane_base + static_cast<uint32_t>(slot * WG_SLOT_COLS + 16 * b), r);
+          tmem_st_32x32b_x16(lane_base + static_cast<uint32_t>(stage * WG_SLOT_COLS + 16 * b), r);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(qempty + stage));   // the codes are in registers
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(afull + slot));
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(afull + stage), lead));
       }
     }
   } else {
@@ -405,15 +445,54 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     const int h0 = (ew >> 2) * half;
     const uint32_t buf = base + g.off_out + static_cast<uint32_t>(ew) * WG_OUT_BUF;
     const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h0);
+    int stage = 0;
     uint32_t aphase = 0;
+    uint32_t dphase = 0;                         // bit s: the phase of ydone[s], which only db tiles use
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < g.units; u += gridDim.x) {
+    for (int u = u0; ok && u < g.units; u += G) {
       const GradUnit t = grad_unit(g, u);
       float sum[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-      for (int s = t.s0; s < t.s1; s += WG_SEG) {
-        if (!mbar_wait_warp(smem_u32(accf), aphase, g.wait, abort_flag)) {
+      const bool with_db = g.db != nullptr && t.kt == 0;
+      // column sums: the warp takes 16 tokens (tw) of every step and one 64-channel chunk (cw; with a single
+      // chunk 8 tokens), a lane the 8 channels of 16-byte unit lane % 8 of every fourth token
+      const int cw = half_n == 128 ? ew >> 2 : 0;
+      const int rows = half_n == 128 ? 16 : 8;
+      const int tw = (half_n == 128 ? ew & 3 : ew) * rows;
+      float col[8] = {};
+      for (int s = t.s0; s < t.s1;) {
+        const int end = min(t.s1, s + WG_SEG);
+        if (with_db) {
+          for (; s < end; ++s) {
+            const bool w = mbar_wait_warp(smem_u32(ydone + stage), (dphase >> stage) & 1u, g.wait, abort_flag);
+            if (w) {
+              const uint32_t sy = base + static_cast<uint32_t>(stage) * y_bytes + static_cast<uint32_t>(cw) * 8192u;
+              for (int j = 0; j < rows; j += 4) {
+                const int m = tw + j + (lane >> 3);
+                const uint4 v = pipe::lds128(sy + pipe::sw128_off(m, lane & 7));
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  col[2 * i] += __uint_as_float(x[i] << 16);
+                  col[2 * i + 1] += __uint_as_float(x[i] & 0xffff0000u);
+                }
+              }
+            }
+            if (!pipe::bar_and(1, 32 * WG_EPI_WARPS, w)) {
+              ok = false;
+              break;
+            }
+            if (ew == 0 && lane == 0) mbar_arrive(smem_u32(yempty + stage));
+            dphase ^= 1u << stage;
+            stage = (stage + 1) % WG_RING;
+          }
+        } else {
+          stage = (stage + end - s) % WG_RING;
+          s = end;
+        }
+        if (!ok) break;
+        if (!pipe::bar_and(1, 32 * WG_EPI_WARPS, mbar_wait_warp(smem_u32(accf), aphase, g.wait, abort_flag))) {
           ok = false;
           break;
         }
@@ -431,11 +510,40 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(acce));
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(acce), lead));
       }
       if (!ok) break;
-      const int k0 = t.kt * 128 + q * 32;
+      const int k0 = t.kt * 256 + static_cast<int>(rank) * 128 + q * 32;
       const int n0 = t.nt * g.bn + h0;
+      if (with_db) {
+        // the four lanes of a unit, then the warps of a chunk, in order; the sums of this CTA's channels go to
+        // db, or for a split beside the partial tile
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          col[i] += __shfl_xor_sync(0xffffffffu, col[i], 8);
+          col[i] += __shfl_xor_sync(0xffffffffu, col[i], 16);
+        }
+        if (lane == 0) bulk_wait_group_read<0>();     // the staging buffer is free
+        __syncwarp();
+        if (lane < 8) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pipe::sts32(buf + static_cast<uint32_t>(lane * 8 + i) * 4u, __float_as_uint(col[i]));
+        }
+        named_bar_sync(1, 32 * WG_EPI_WARPS);
+        const int c = threadIdx.x - 32 * WG_EPI_WARP0;     // channel of this CTA's half
+        float v = 0.0f;
+        if (c < half_n) {
+          const int nw = half_n == 128 ? 4 : 8, w0 = (c >> 6) * 4;
+          for (int w = 0; w < nw; ++w)
+            v += __uint_as_float(pipe::lds32(base + g.off_out + static_cast<uint32_t>((w0 + w) * WG_OUT_BUF + (c & 63) * 4)));
+        }
+        named_bar_sync(1, 32 * WG_EPI_WARPS);              // read before the buffers are used again
+        if (c < half_n) {
+          const int n = t.nt * g.bn + static_cast<int>(rank) * half_n + c;
+          if (g.splits > 1) pipe::sts32(base + g.off_out + static_cast<uint32_t>(c) * 4u, __float_as_uint(v));
+          else if (n < g.N) g.db[n] = g.accumulate ? g.db[n] + v : v;
+        }
+      }
       if (g.splits > 1) {
         // fp32 partial [channel][feature] over the dY ring (the CTA's only unit: its last accumulator is
         // complete, so every stage has been consumed)
@@ -493,11 +601,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   // at once) could take what the epilogue's own growth still waits for.
   if (warp < WG_EPI_WARP0) set_regs_up<WG_REGS>();
   else set_regs_down<WG_REGS>();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  cluster_sync_all();            // no CTA leaves while its peer may still signal it; partials are in place
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
 
   if (g.splits > 1) {
-    cluster_sync_all();
-    const GradUnit t = grad_unit(g, blockIdx.x);
+    // split s of the tile and this rank of its pair is the cluster's CTA 2 s + rank
+    const GradUnit t = grad_unit(g, u0);
     const int rows = (g.bn + g.splits - 1) / g.splits;
     const int r0 = t.split * rows;
     const int r1 = min(g.bn, r0 + rows);
@@ -505,12 +614,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       const int ch = r0 + (i >> 5);
       const int quad = i & 31;
       const int n = t.nt * g.bn + ch;
-      const int k = t.kt * 128 + 4 * quad;
+      const int k = t.kt * 256 + static_cast<int>(rank) * 128 + 4 * quad;
       if (n >= g.N || k >= g.K) continue;              // K % 16 == 0: the quad is all in or all out
       const uint32_t off = base + static_cast<uint32_t>(ch * 128 + 4 * quad) * 4u;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int sp = 0; sp < g.splits; ++sp) {
-        const float4 v = ld_shared_cluster_f4(map_to_rank(off, static_cast<uint32_t>(sp)));
+        const float4 v = ld_shared_cluster_f4(map_to_rank(off, static_cast<uint32_t>(2 * sp) + rank));
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
@@ -529,98 +638,25 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
       }
     }
+    if (g.db != nullptr && t.kt == 0 && t.split == 0 && static_cast<int>(threadIdx.x) < half_n / 4) {
+      const int n = t.nt * g.bn + static_cast<int>(rank) * half_n + 4 * static_cast<int>(threadIdx.x);
+      if (n < g.N) {                                   // N % 8 == 0
+        const uint32_t off = base + g.off_out + threadIdx.x * 16u;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int sp = 0; sp < g.splits; ++sp) {
+          const float4 v = ld_shared_cluster_f4(map_to_rank(off, static_cast<uint32_t>(2 * sp) + rank));
+          s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        float4* p = reinterpret_cast<float4*>(g.db + n);
+        if (g.accumulate) {
+          const float4 v = *p;
+          s = make_float4(v.x + s.x, v.y + s.y, v.z + s.z, v.w + s.w);
+        }
+        *p = s;
+      }
+    }
     cluster_sync_all();
   }
-}
-
-// db[n] (+)= sum_m dY[m, n]: a cluster of CTAs shares 64 channels, each CTA a
-// contiguous run of tokens; a thread sums 8 channels of every 32nd token in
-// fp32, the 32 partial sums and then the CTAs' sums are added in order.  One
-// read of dY at HBM rate.
-constexpr int DB_THREADS = 256;
-__global__ void __launch_bounds__(DB_THREADS) bias_grad_kernel(const uint16_t* __restrict__ dy, int M, int N, int64_t ld,
-                                                               int accumulate, float* __restrict__ db) {
-  __shared__ __align__(16) float part[32][64];
-  __shared__ __align__(16) float tot[64];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int S = static_cast<int>(gridDim.y);
-  const int split = static_cast<int>(blockIdx.y);
-  const int n0 = blockIdx.x * 64 + (threadIdx.x & 7) * 8;
-  const int r = threadIdx.x >> 3;
-  const int m0 = static_cast<int>(static_cast<int64_t>(split) * M / S);
-  const int m1 = static_cast<int>(static_cast<int64_t>(split + 1) * M / S);
-  float a[8] = {};
-  if (n0 < N) {                                          // N % 8 == 0
-    for (int m = m0 + r; m < m1; m += 32) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(dy + m * ld + n0));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[2 * i] += __uint_as_float(w[i] << 16);
-        a[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) part[r][(threadIdx.x & 7) * 8 + i] = a[i];
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    float s = 0.0f;
-    for (int i = 0; i < 32; ++i) s += part[i][threadIdx.x];
-    tot[threadIdx.x] = s;
-  }
-  if (S > 1) cluster_sync_all();
-  else __syncthreads();
-  if (split == 0 && threadIdx.x < 16) {
-    const int n = blockIdx.x * 64 + threadIdx.x * 4;
-    if (n < N) {
-      const uint32_t off = smem_u32(tot) + threadIdx.x * 16u;
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int sp = 0; sp < S; ++sp) {
-        float4 v;
-        if (S > 1) v = ld_shared_cluster_f4(map_to_rank(off, static_cast<uint32_t>(sp)));
-        else v = *reinterpret_cast<const float4*>(tot + threadIdx.x * 4);
-        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-      }
-      float4* p = reinterpret_cast<float4*>(db + n);
-      if (accumulate) {
-        const float4 v = *p;
-        s = make_float4(v.x + s.x, v.y + s.y, v.z + s.z, v.w + s.w);
-      }
-      *p = s;
-    }
-  }
-  if (S > 1) cluster_sync_all();                         // the sums have been read
-}
-
-template <typename... P, typename... A>
-dq_status launch(void (*kernel)(P...), dim3 grid, int threads, int smem, dim3 cluster, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster.x;
-  attr[1].val.clusterDim.y = cluster.y;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster.x * cluster.y > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-  return e == cudaSuccess ? DQ_OK : cuda_fail(e);
-}
-
-dq_status launch_bias_grad(const uint16_t* dy, int64_t M, int64_t N, int64_t ld, int accumulate, float* db, int sm_count,
-                           cudaStream_t stream) {
-  const int groups = static_cast<int>((N + 63) / 64);
-  int S = 1;
-  while (S < 8 && groups * S < 4 * sm_count && M / (2 * S) >= 64) S *= 2;
-  return launch(bias_grad_kernel, dim3(groups, S), DB_THREADS, 0, dim3(1, S), stream, dy, static_cast<int>(M),
-                static_cast<int>(N), ld, accumulate, db);
 }
 
 }  // namespace
@@ -654,24 +690,25 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
     return e == cudaSuccess ? DQ_OK : cuda_fail(e);
   }
   const auto* dy = static_cast<const uint16_t*>(dy_bf16);
-  if (db != nullptr && (st = launch_bias_grad(dy, M, N, lddy, accumulate, db, dev->sm_count, cs)) != DQ_OK) return st;
 
   GradArgs g = {};
   g.M = static_cast<int>(M);
   g.N = static_cast<int>(N);
   g.K = static_cast<int>(K);
-  g.kt = static_cast<int>((K + 127) / 128);
+  g.kt = static_cast<int>((K + 255) / 256);
   g.ks = static_cast<int>((M + WG_STEP - 1) / WG_STEP);
-  // Tile width and split with the least estimated time: waves of steps, a step
-  // costing about 0.25 + bn / 1280 us, plus a few us per unit for its ends.
+  int pairs = 0;
+  if ((st = pair_slots(*dev, &pairs)) != DQ_OK) return st;
+  // Tile width and split with the least estimated time: waves of steps, plus a
+  // few us per unit for its ends.
   int64_t tiles = 0;
   double best = 1e300;
-  for (int bn = 64; bn <= 256; bn += 64) {
+  for (int bn = 128; bn <= 256; bn += 128) {
     const int64_t nt = (N + bn - 1) / bn, n = nt * g.kt;
-    for (int sp = 1; sp <= 8; sp *= 2) {
-      if (sp > 1 && (n * sp > dev->sm_count || g.ks < 2 * sp)) break;
-      const double waves = static_cast<double>((n * sp + dev->sm_count - 1) / dev->sm_count);
-      const double cost = waves * (((g.ks + sp - 1) / sp) * (0.25 + bn / 1280.0) + 2.0) + (sp > 1 ? 1.0 + 0.2 * sp : 0.0);
+    for (int sp = 1; sp <= 4; sp *= 2) {
+      if (sp > 1 && (n * sp > pairs || g.ks < 2 * sp)) break;
+      const double waves = static_cast<double>((n * sp + pairs - 1) / pairs);
+      const double cost = waves * (((g.ks + sp - 1) / sp) * (bn == 256 ? 0.33 : 0.25) + 2.0) + (sp > 1 ? 1.0 + 0.2 * sp : 0.0);
       if (cost < best) {
         best = cost;
         g.bn = bn;
@@ -681,24 +718,24 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
       }
     }
   }
-  if (tiles > 0x3fffffff) return DQ_ERR_UNSUPPORTED;
+  if (tiles > 0x1fffffff) return DQ_ERR_UNSUPPORTED;
   g.units = static_cast<int>(tiles) * g.splits;
   g.full_chunks = static_cast<int>(N / 64);
-  // Five stages of dY at 256 channels, the rest of the shared memory for codes.
-  // The rings that the two converter groups share have an even length, so that
-  // a stage belongs to one group: a parity wait cannot tell a lap from the one
-  // two before it, and a group that ran ahead of the other could take its
-  // stage's next lap for landed.
-  const int room = 227 * 1024 - 1024 - WG_EPI_WARPS * WG_OUT_BUF - WG_BAR_BYTES;
-  g.stages = std::min(WG_MAX_RING, (room - 6 * WG_CODE_STAGE) / (g.bn * 128));
-  g.code_stages = std::min(WG_MAX_RING, (room - g.stages * g.bn * 128) / WG_CODE_STAGE) & ~1;
-  g.slots = std::min(WG_MAX_RING, (512 - g.bn) / WG_SLOT_COLS) & ~1;
   // (the swizzle of the output blocks counts from 1024-byte boundaries)
-  g.off_out = static_cast<uint32_t>(g.stages * g.bn * 128);
+  g.off_out = static_cast<uint32_t>(WG_RING * g.bn * 64);
   g.off_q = g.off_out + WG_EPI_WARPS * WG_OUT_BUF;
-  g.off_bar = g.off_q + static_cast<uint32_t>(g.code_stages * WG_CODE_STAGE);
+  g.off_bar = g.off_q + WG_RING * WG_CODE_STAGE;
   const int smem = static_cast<int>(g.off_bar) + WG_BAR_BYTES + 1024;
+  static_assert(WG_RING * 256 * 64 + WG_EPI_WARPS * WG_OUT_BUF + WG_RING * WG_CODE_STAGE + WG_BAR_BYTES + 1024 <= 227 * 1024,
+                "shared memory");
+  static_assert(256 + WG_RING * WG_SLOT_COLS <= 512, "tensor memory");
+  // The converter groups share the code and slot rings: with an even length a
+  // stage belongs to one group (a parity wait cannot tell a lap from the one
+  // two before it, and a group that ran ahead of the other could take its
+  // stage's next lap for landed).
+  static_assert(WG_RING % 2 == 0, "ring length");
   g.dw = dw;
+  g.db = db;
   g.f32 = f32;
   g.accumulate = accumulate != 0;
   g.wait = WaitCtl{dev->err_word, wait_timeout_ns()};
@@ -710,7 +747,7 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
     return st;
   y3 = y2;
   if (g.full_chunks > 0 &&
-      (st = make_tmap_chunks(&y3, dy, M, g.full_chunks, static_cast<uint64_t>(lddy) * 2, WG_STEP, g.bn / 64)) != DQ_OK)
+      (st = make_tmap_chunks(&y3, dy, M, g.full_chunks, static_cast<uint64_t>(lddy) * 2, WG_STEP, g.bn / 128)) != DQ_OK)
     return st;
   if ((st = make_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT64, codes, static_cast<uint64_t>(K) * 2, 2 * groups,
                          static_cast<uint64_t>(K) * 16, 256, 4, 0)) != DQ_OK)
@@ -724,9 +761,22 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
   }
   if (st != DQ_OK) return st;
   if ((st = smem_limit_once(reinterpret_cast<const void*>(&act8_grad_kernel), smem)) != DQ_OK) return st;
-  const unsigned grid = g.splits > 1 ? static_cast<unsigned>(g.units)
-                                     : static_cast<unsigned>(std::min<int64_t>(tiles, dev->sm_count));
-  return launch(act8_grad_kernel, dim3(grid), WG_THREADS, smem, dim3(g.splits, 1), cs, y3, y2, tq, te, tc, g);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (g.splits > 1 ? g.units : std::min(pairs, g.units))));
+  cfg.blockDim = dim3(WG_THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = cs;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(2 * g.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, act8_grad_kernel, y3, y2, tq, te, tc, g);
+  return e == cudaSuccess ? DQ_OK : cuda_fail(e);
 }
 
 }  // extern "C"
