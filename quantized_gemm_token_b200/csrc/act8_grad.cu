@@ -28,7 +28,7 @@
 // converted steps in tensor memory.
 // Sums: the tensor core truncates when it adds to its accumulator, so a chain
 // of MMAs loses about 2^-26 of the sum per instruction, all in one direction
-// (65792 tokens in one chain: 4.4e-5 of the result).  Every 1024 tokens the
+// (65792 tokens in one chain: 4.4e-5 of the result).  Every 2048 tokens the
 // epilogue adds the accumulator to fp32 registers (rounding to nearest) and
 // the chain starts anew; the converted steps in flight cover the read.
 // db: in the tiles of the first 256 features the epilogue warps also add up
@@ -59,7 +59,7 @@ constexpr int WG_EPI_WARPS = 8;
 constexpr int WG_REGS = 96;
 constexpr int WG_REGS_ISSUE = 40, WG_REGS_CVT = 56, WG_REGS_EPI = 160;
 constexpr int WG_STEP = 64;                  // tokens per step
-constexpr int WG_SEG = 16;                   // steps per accumulator chain
+constexpr int WG_SEG = 32;                   // steps per accumulator chain
 constexpr int WG_CODES = 128 * WG_STEP;      // bytes: [4 x 16 tokens][128 features][16]
 constexpr int WG_RING = 8;                   // stages or slots of each ring
 constexpr int WG_CODE_STAGE = WG_CODES + 256;
@@ -116,7 +116,7 @@ __device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
 }
 
 // Arrive on the mbarrier at shared::cluster address `bar` for tensor-memory
-// writes (waited for, and fenced by tcgen05.fence::before_thread_sync): they
+// accesses (waited for, and fenced by tcgen05.fence::before_thread_sync): they
 // are not ordered by the arrive itself, so it needs no release (which at
 // cluster scope takes more than the 512 cycles of a step).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
@@ -499,18 +499,18 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         aphase ^= 1;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (16 * c < half) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(tb + 16 * c, r);
+        for (int c = 0; c < 4; ++c) {
+          if (32 * c < half) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tb + 32 * c, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[16 * c + j] += __uint_as_float(r[j]);
+            for (int j = 0; j < 32; ++j) sum[32 * c + j] += __uint_as_float(r[j]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(acce), lead));
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(acce), lead));
       }
       if (!ok) break;
       const int k0 = t.kt * 256 + static_cast<int>(rank) * 128 + q * 32;
