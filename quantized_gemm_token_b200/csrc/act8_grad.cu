@@ -41,6 +41,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -54,10 +55,11 @@ constexpr int WG_THREADS = 640;
 constexpr int WG_CVT_WARP0 = 4;              // warps 4..11: two converter groups
 constexpr int WG_EPI_WARP0 = 12;             // warps 12..19
 constexpr int WG_EPI_WARPS = 8;
-// registers per thread of the five warpgroups: 40 + 2 * 56 + 2 * 160 = 472, of
+// registers per thread of the five warpgroups: 32 + 2 * 56 + 2 * 168 = 480, of
 // the 5 * 96 = 480 that the block is launched with; at the end all go back to 96
 constexpr int WG_REGS = 96;
-constexpr int WG_REGS_ISSUE = 40, WG_REGS_CVT = 56, WG_REGS_EPI = 160;
+constexpr int WG_REGS_ISSUE = 32, WG_REGS_CVT = 56, WG_REGS_EPI = 168;
+static_assert(WG_REGS_ISSUE + 2 * WG_REGS_CVT + 2 * WG_REGS_EPI <= 5 * WG_REGS, "register split");
 constexpr int WG_STEP = 64;                  // tokens per step
 constexpr int WG_SEG = 32;                   // steps per accumulator chain
 constexpr int WG_CODES = 128 * WG_STEP;      // bytes: [4 x 16 tokens][128 features][16]
@@ -66,12 +68,15 @@ constexpr int WG_CODE_STAGE = WG_CODES + 256;
 constexpr int WG_BAR_BYTES = 512;
 constexpr int WG_OUT_BUF = 2048;             // per epilogue warp: 32 x 32 bf16 or 16 x 32 fp32
 constexpr int WG_SLOT_COLS = WG_STEP / 2;    // TMEM columns of one converted step
+constexpr int WG_MAX_SMEM = WG_RING * 256 * 64 + WG_EPI_WARPS * WG_OUT_BUF + WG_RING * WG_CODE_STAGE + WG_BAR_BYTES + 1024;
+static_assert(WG_MAX_SMEM <= 227 * 1024, "shared memory");
 constexpr int64_t kGradMaxDim = int64_t(1) << 30;
 
 struct GradArgs {
   int M, N, K;
   int bn;                  // channels per tile (128 or 256), half of them per CTA
   int kt, nt;              // feature tiles (256), channel tiles
+  int tile0;               // first tile of this launch
   int splits, units;
   int ks;                  // token steps: ceil(M / 64)
   int full_chunks;         // N / 64: chunks the 3-D map covers
@@ -191,10 +196,18 @@ struct GradUnit {
 };
 __device__ __forceinline__ GradUnit grad_unit(const GradArgs& g, int u) {
   GradUnit t;
-  const int tile = u / g.splits;
+  int tile = u / g.splits;
   t.split = u - tile * g.splits;
-  t.nt = tile / g.kt;
-  t.kt = tile - t.nt * g.kt;
+  tile += g.tile0;
+  if (g.db != nullptr) {
+    // the tiles that also sum columns (kt = 0, the slowest) come last, where a
+    // partial wave is split
+    t.kt = g.kt - 1 - tile / g.nt;
+    t.nt = tile % g.nt;
+  } else {
+    t.nt = tile / g.kt;
+    t.kt = tile - t.nt * g.kt;
+  }
   t.s0 = static_cast<int>(static_cast<int64_t>(t.split) * g.ks / g.splits);
   t.s1 = static_cast<int>(static_cast<int64_t>(t.split + 1) * g.ks / g.splits);
   return t;
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     *abort_flag = 0;
     for (int i = 0; i < WG_RING; ++i) {
       mbar_init(smem_u32(yfull + i), 1);
-      mbar_init(smem_u32(yempty + i), 1);
+      mbar_init(smem_u32(yempty + i), g.db != nullptr ? 2 : 1);
       mbar_init(smem_u32(qfull + i), 1);
       mbar_init(smem_u32(qempty + i), 4);
       mbar_init(smem_u32(afull + i), 8);
@@ -336,7 +349,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       bool ok = true, tested = false;             // tested: the next step's operands were found ready
       for (int u = u0; ok && u < g.units; u += G) {
         const GradUnit t = grad_unit(g, u);
+        // a stage is freed by the MMAs, or in db tiles by the two warps that sum it
         uint64_t* const ynext = g.db != nullptr && t.kt == 0 ? ydone : yempty;
+        const bool twice = g.db != nullptr && t.kt != 0;
         for (int s = t.s0; ok && s < t.s1;) {
           const int end = min(t.s1, s + WG_SEG);
           if (!mbar_wait_warp(smem_u32(acce), aphase ^ 1, g.wait, abort_flag)) {
@@ -365,6 +380,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
               for (int j = 0; j < 4; ++j)      // 16 tokens: 8 columns of A, 2048 bytes of B
                 mma_bf16_ts_pair(tmem, a + 8 * j, bd + 128 * j, idesc, (s > first || j > 0) ? 1u : 0u);
               commit_pair(yb, mask);
+              if (twice) commit_pair(yb, mask);
               commit_pair(ab, mask);
             }
             __syncwarp();
@@ -455,44 +471,47 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
 #pragma unroll
       for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
       const bool with_db = g.db != nullptr && t.kt == 0;
-      // column sums: the warp takes 16 tokens (tw) of every step and one 64-channel chunk (cw; with a single
-      // chunk 8 tokens), a lane the 8 channels of 16-byte unit lane % 8 of every fourth token
-      const int cw = half_n == 128 ? ew >> 2 : 0;
-      const int rows = half_n == 128 ? 16 : 8;
-      const int tw = (half_n == 128 ? ew & 3 : ew) * rows;
+      // Column sums: warps w and w + 4 take the steps of ring stages w and w + 4,
+      // half of a step's tokens each (so four steps are summed at a time), a
+      // lane the 8 channels of 16-byte unit lane % (units per row) of every
+      // second (or fourth) token.
+      const int unit = lane & (half_n / 8 - 1);
+      const int tstep = 256 / half_n;
+      const int tok0 = lane / (half_n / 8) + (ew >> 2) * (WG_STEP / 2);
       float col[8] = {};
+      auto sum_stage = [&](int st) {             // false: the wait failed
+        if (!mbar_wait_warp(smem_u32(ydone + st), (dphase >> st) & 1u, g.wait, abort_flag)) return false;
+        dphase ^= 1u << st;
+        const uint32_t sy = base + static_cast<uint32_t>(st) * y_bytes + static_cast<uint32_t>(unit >> 3) * 8192u;
+#pragma unroll 4
+        for (int m = 0; m < WG_STEP / 2; m += tstep) {
+          const uint4 v = pipe::lds128(sy + pipe::sw128_off(tok0 + m, unit & 7));
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            col[2 * i] += __uint_as_float(x[i] << 16);
+            col[2 * i + 1] += __uint_as_float(x[i] & 0xffff0000u);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(yempty + st));
+        return true;
+      };
       for (int s = t.s0; s < t.s1;) {
         const int end = min(t.s1, s + WG_SEG);
+        // this warp's steps of the chain: all but its last now, that one after the accumulator is read
+        int last = -1;
         if (with_db) {
-          for (; s < end; ++s) {
-            const bool w = mbar_wait_warp(smem_u32(ydone + stage), (dphase >> stage) & 1u, g.wait, abort_flag);
-            if (w) {
-              const uint32_t sy = base + static_cast<uint32_t>(stage) * y_bytes + static_cast<uint32_t>(cw) * 8192u;
-              for (int j = 0; j < rows; j += 4) {
-                const int m = tw + j + (lane >> 3);
-                const uint4 v = pipe::lds128(sy + pipe::sw128_off(m, lane & 7));
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  col[2 * i] += __uint_as_float(x[i] << 16);
-                  col[2 * i + 1] += __uint_as_float(x[i] & 0xffff0000u);
-                }
-              }
-            }
-            if (!pipe::bar_and(1, 32 * WG_EPI_WARPS, w)) {
-              ok = false;
-              break;
-            }
-            if (ew == 0 && lane == 0) mbar_arrive(smem_u32(yempty + stage));
-            dphase ^= 1u << stage;
-            stage = (stage + 1) % WG_RING;
+          for (int i = s + ((ew - stage) & 3); ok && i < end; i += 4) {
+            const int st = (stage + i - s) & (WG_RING - 1);
+            if (i + 4 < end) ok = sum_stage(st);
+            else last = st;
           }
-        } else {
-          stage = (stage + end - s) % WG_RING;
-          s = end;
         }
-        if (!ok) break;
-        if (!pipe::bar_and(1, 32 * WG_EPI_WARPS, mbar_wait_warp(smem_u32(accf), aphase, g.wait, abort_flag))) {
+        stage = (stage + end - s) & (WG_RING - 1);
+        s = end;
+        ok = ok && mbar_wait_warp(smem_u32(accf), aphase, g.wait, abort_flag);
+        if (!pipe::bar_and(1, 32 * WG_EPI_WARPS, ok)) {
           ok = false;
           break;
         }
@@ -511,32 +530,33 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(acce), lead));
+        if (last >= 0) ok = sum_stage(last);
       }
-      if (!ok) break;
+      if (!pipe::bar_and(1, 32 * WG_EPI_WARPS, ok)) {
+        ok = false;
+        break;
+      }
       const int k0 = t.kt * 256 + static_cast<int>(rank) * 128 + q * 32;
       const int n0 = t.nt * g.bn + h0;
       if (with_db) {
-        // the four lanes of a unit, then the warps of a chunk, in order; the sums of this CTA's channels go to
-        // db, or for a split beside the partial tile
+        // the lanes of a unit, then the eight warps in order; the sums of this CTA's channels go to db, or for
+        // a split beside the partial tile
+        for (int o = half_n / 8; o < 32; o *= 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          col[i] += __shfl_xor_sync(0xffffffffu, col[i], 8);
-          col[i] += __shfl_xor_sync(0xffffffffu, col[i], 16);
+          for (int i = 0; i < 8; ++i) col[i] += __shfl_xor_sync(0xffffffffu, col[i], o);
         }
         if (lane == 0) bulk_wait_group_read<0>();     // the staging buffer is free
         __syncwarp();
-        if (lane < 8) {
+        if (lane < half_n / 8) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) pipe::sts32(buf + static_cast<uint32_t>(lane * 8 + i) * 4u, __float_as_uint(col[i]));
         }
         named_bar_sync(1, 32 * WG_EPI_WARPS);
         const int c = threadIdx.x - 32 * WG_EPI_WARP0;     // channel of this CTA's half
         float v = 0.0f;
-        if (c < half_n) {
-          const int nw = half_n == 128 ? 4 : 8, w0 = (c >> 6) * 4;
-          for (int w = 0; w < nw; ++w)
-            v += __uint_as_float(pipe::lds32(base + g.off_out + static_cast<uint32_t>((w0 + w) * WG_OUT_BUF + (c & 63) * 4)));
-        }
+        if (c < half_n)
+          for (int w = 0; w < WG_EPI_WARPS; ++w)
+            v += __uint_as_float(pipe::lds32(base + g.off_out + static_cast<uint32_t>(w * WG_OUT_BUF + c * 4)));
         named_bar_sync(1, 32 * WG_EPI_WARPS);              // read before the buffers are used again
         if (c < half_n) {
           const int n = t.nt * g.bn + static_cast<int>(rank) * half_n + c;
@@ -659,6 +679,44 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   }
 }
 
+std::atomic<int> g_grad_clusters[64][3] = {};
+
+cudaLaunchConfig_t grad_config(cudaLaunchAttribute (&attr)[2], int splits, int smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(WG_THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(2 * splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of `splits` (1, 2 or 4) pairs that fit on the device at once, one
+// CTA per SM (an SM count that is no multiple of the cluster size in a GPC
+// leaves SMs idle).
+dq_status grad_clusters(const DeviceInfo& d, int splits, int* out) {
+  std::atomic<int>& slot = g_grad_clusters[d.device & 63][splits == 1 ? 0 : splits == 2 ? 1 : 2];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = grad_config(attr, splits, WG_MAX_SMEM, nullptr);
+    cfg.numAttrs = 1;                                     // the cluster shape only
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * splits * (d.sm_count / (2 * splits))));
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, act8_grad_kernel, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e);
+    n = n < 1 ? 1 : n;
+    slot.store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return DQ_OK;
+}
+
 }  // namespace
 }  // namespace dq
 
@@ -697,37 +755,43 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
   g.K = static_cast<int>(K);
   g.kt = static_cast<int>((K + 255) / 256);
   g.ks = static_cast<int>((M + WG_STEP - 1) / WG_STEP);
-  int pairs = 0;
-  if ((st = pair_slots(*dev, &pairs)) != DQ_OK) return st;
-  // Tile width and split with the least estimated time: waves of steps, plus a
-  // few us per unit for its ends.
+  if ((st = smem_limit_once(reinterpret_cast<const void*>(&act8_grad_kernel), WG_MAX_SMEM)) != DQ_OK) return st;
+  int fit[3];                                             // clusters of 1, 2 and 4 pairs
+  for (int i = 0; i < 3; ++i)
+    if ((st = grad_clusters(*dev, 1 << i, fit + i)) != DQ_OK) return st;
+  const int pairs = fit[0];
+  // Tile width with the least estimated time, in steps: whole waves of tiles,
+  // then the remaining tiles with their tokens split over 2 or 4 pairs where
+  // that still fits in one wave (a launch of its own).
   int64_t tiles = 0;
+  int rest = 0, rest_splits = 1;
   double best = 1e300;
   for (int bn = 128; bn <= 256; bn += 128) {
     const int64_t nt = (N + bn - 1) / bn, n = nt * g.kt;
+    const double step = bn == 256 ? 0.31 : 0.24, ends = 4.0;       // us
+    const int64_t waves = n / pairs, r = n % pairs;
     for (int sp = 1; sp <= 4; sp *= 2) {
-      if (sp > 1 && (n * sp > pairs || g.ks < 2 * sp)) break;
-      const double waves = static_cast<double>((n * sp + pairs - 1) / pairs);
-      const double cost = waves * (((g.ks + sp - 1) / sp) * (bn == 256 ? 0.33 : 0.25) + 2.0) + (sp > 1 ? 1.0 + 0.2 * sp : 0.0);
-      if (cost < best) {
+      if (sp > 1 && (r == 0 || r > fit[sp / 2] || g.ks < 4 * sp)) break;
+      const double cost = static_cast<double>(waves) * (g.ks * step + ends) +
+                          (r > 0 ? (g.ks + sp - 1) / sp * step + ends : 0.0) +
+                          (sp > 1 ? (waves > 0 ? 10.0 : 5.0) : 0.0);   // the join, and a second launch
+      if (cost < 0.98 * best) {
         best = cost;
         g.bn = bn;
         g.nt = static_cast<int>(nt);
-        g.splits = sp;
         tiles = n;
+        rest = sp > 1 ? static_cast<int>(r) : 0;
+        rest_splits = sp;
       }
     }
   }
   if (tiles > 0x1fffffff) return DQ_ERR_UNSUPPORTED;
-  g.units = static_cast<int>(tiles) * g.splits;
   g.full_chunks = static_cast<int>(N / 64);
   // (the swizzle of the output blocks counts from 1024-byte boundaries)
   g.off_out = static_cast<uint32_t>(WG_RING * g.bn * 64);
   g.off_q = g.off_out + WG_EPI_WARPS * WG_OUT_BUF;
   g.off_bar = g.off_q + WG_RING * WG_CODE_STAGE;
   const int smem = static_cast<int>(g.off_bar) + WG_BAR_BYTES + 1024;
-  static_assert(WG_RING * 256 * 64 + WG_EPI_WARPS * WG_OUT_BUF + WG_RING * WG_CODE_STAGE + WG_BAR_BYTES + 1024 <= 227 * 1024,
-                "shared memory");
   static_assert(256 + WG_RING * WG_SLOT_COLS <= 512, "tensor memory");
   // The converter groups share the code and slot rings: with an even length a
   // stage belongs to one group (a parity wait cannot tell a lap from the one
@@ -760,23 +824,19 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
                       static_cast<uint64_t>(K) * 2, 64, 32, 0);
   }
   if (st != DQ_OK) return st;
-  if ((st = smem_limit_once(reinterpret_cast<const void*>(&act8_grad_kernel), smem)) != DQ_OK) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (g.splits > 1 ? g.units : std::min(pairs, g.units))));
-  cfg.blockDim = dim3(WG_THREADS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = cs;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(2 * g.splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, act8_grad_kernel, y3, y2, tq, te, tc, g);
-  return e == cudaSuccess ? DQ_OK : cuda_fail(e);
+  auto run = [&](int tile0, int count, int splits) {
+    g.tile0 = tile0;
+    g.splits = splits;
+    g.units = count * splits;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = grad_config(attr, splits, smem, cs);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (splits > 1 ? g.units : std::min(pairs, g.units))));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, act8_grad_kernel, y3, y2, tq, te, tc, g);
+    return e == cudaSuccess ? DQ_OK : cuda_fail(e);
+  };
+  const int whole = static_cast<int>(tiles) - rest;
+  if (whole > 0 && (st = run(0, whole, 1)) != DQ_OK) return st;
+  return rest > 0 ? run(whole, rest, rest_splits) : DQ_OK;
 }
 
 }  // extern "C"
