@@ -61,6 +61,12 @@ KERNEL_SOURCES = {
     "dq_hqq_linear": ("hqq.cu", "pipeline.cuh", "sm100.cuh", "host.cu", "internal.h"),
     "dq_s24_int8_linear": ("sparse24.cu", "pipeline.cuh", "sm100.cuh", "host.cu", "internal.h"),
     "dq_hqq_linear_t": ("hqq.cu", "pipeline.cuh", "sm100.cuh", "host.cu", "internal.h"),
+    "dq_quantize_rows_fp4": ("fp4_quant.cu", "mx.h", "sm100.cuh", "host.cu", "internal.h"),
+    "dq_fp4_linear": ("fp4.cu", "mx_host.cu", "mx.cuh", "mx.h", "gemm_common.cuh", "pipeline.cuh", "sm100.cuh", "host.cu",
+                      "internal.h"),
+    "dq_act8_pack": ("act8.cu", "mx.h", "sm100.cuh", "host.cu", "internal.h"),
+    "dq_act8_weight_grad": ("act8_grad.cu", "mx_host.cu", "mx.cuh", "mx.h", "gemm_common.cuh", "pipeline.cuh",
+                            "sm100.cuh", "host.cu", "internal.h"),
 }
 
 

@@ -1,4 +1,6 @@
-"""Python binding of libdq: the int8 dynamic-quantization linear layer on B200.
+"""Python binding of libdq: the int8 dynamic-quantization linear layer on B200,
+its FP8, 2:4, int4 and microscaled 4-bit siblings, and the 8-bit activation
+checkpoints from which a layer's weight gradient is computed.
 
 Argument marshalling only.  Every step of the layer runs in libdq's CUDA
 kernels (``csrc/``); PyTorch supplies device memory and streams.  There is no
@@ -678,6 +680,20 @@ def _fp4_scale_shape(rows: int, K: int, code: int):
     return ((rows + 127) // 128, (K + g - 1) // g, 512)
 
 
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """torch.empty on like's device (with the strides spelt out: three quarters
+    of the host time), belonging to the stream that the call's kernel runs on,
+    so that the caching allocator does not hand it out again under the kernel."""
+    if stream is not None:
+        with torch.cuda.stream(_stream_obj(stream)):
+            return _new(shape, dtype, like, None)
+    if len(shape) == 2:
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
+    if len(shape) == 3:
+        return torch.empty_strided(shape, (shape[1] * shape[2], shape[2], 1), dtype=dtype, device=like.device)
+    return torch.empty_strided(shape, (1,), dtype=dtype, device=like.device)
+
+
 def _here(t: torch.Tensor, name: str) -> int:
     """The device index of a call's first tensor, which must be the current
     device (a kernel is launched there)."""
@@ -737,18 +753,18 @@ def _quantize_fp4(fn, name, x, dtype, fmt, q, sf, s, stream):
     shape = _fp4_scale_shape(M, K, code)
     ldq = K // 2
     if q is None:
-        q = x.new_empty((M, K // 2), dtype=torch.uint8)
+        q = _new((M, K // 2), torch.uint8, x, stream)
     else:
         if _here(q, "q") != dev or _rows(q, torch.uint8, "q")[:2] != (M, K // 2):
             raise ValueError(f"q must be {(M, K // 2)}")
         ldq = _rows(q, torch.uint8, "q")[2]
     if sf is None:
-        sf = x.new_empty(shape, dtype=torch.uint8)
+        sf = _new(shape, torch.uint8, x, stream)
     else:
         _arg(sf, torch.uint8, shape, dev, "sf")
     if code == DQ_FP4_NV:
         if s is None:
-            s = x.new_empty((M,), dtype=torch.float32)
+            s = _new((M,), torch.float32, x, stream)
         else:
             _arg(s, torch.float32, (M,), dev, "row scales")
     elif s is not None:
@@ -786,7 +802,7 @@ def dq_fp4_tile_scales(scales: torch.Tensor, fmt="nv", sf: torch.Tensor = None, 
         raise ValueError("scales: a row must hold the scales of a positive multiple of 32 features")
     shape = _fp4_scale_shape(R, K, code)
     if sf is None:
-        sf = scales.new_empty(shape)
+        sf = _new(shape, torch.uint8, scales, stream)
     _arg(sf, torch.uint8, shape, dev, "sf")
     _check(lib.dq_fp4_tile_scales(_ptr(scales), R, K, code, _ptr(sf), _stream(stream)), "dq_fp4_tile_scales")
     return sf
@@ -812,7 +828,7 @@ def dq_fp4_dequantize(q, sf, s=None, fmt="nv", out=None, stream=None) -> torch.T
     dev = _here(q, "q")
     M, K = _fp4_operand(q, sf, s, code, dev, "q")
     if out is None:
-        out = q.new_empty((M, K), dtype=torch.bfloat16)
+        out = _new((M, K), torch.bfloat16, q, stream)
     else:
         _arg(out, torch.bfloat16, (M, K), dev, "out")
     _check(lib.dq_fp4_dequantize(q.data_ptr(), sf.data_ptr(), _ptr(s), M, K, code, out.data_ptr(), _stream(stream)),
@@ -843,7 +859,7 @@ def dq_fp4_linear(A, sfa, s_row, W, sfw, s_col, bias=None, fmt="nv", out=None, o
     if bias is not None:
         _arg(bias, torch.bfloat16, (N,), dev, "bias")
     if out is None:
-        out = A.new_empty((M, N), dtype=odt)
+        out = _new((M, N), odt, A, stream)
     else:
         _arg(out, odt, (M, N), dev, "out")
     _check(lib.dq_fp4_linear(A.data_ptr(), sfa.data_ptr(), _ptr(s_row), M, K, W.data_ptr(), sfw.data_ptr(),
@@ -875,11 +891,11 @@ def dq_act8_pack(x: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tens
         raise ValueError(f"x: the row length must be a positive multiple of 16, got {K}")
     g = (M + 31) // 32
     if codes is None:
-        codes = x.new_empty((2 * g, K, 16), dtype=torch.int8)
+        codes = _new((2 * g, K, 16), torch.int8, x, stream)
     else:
         _arg(codes, torch.int8, (2 * g, K, 16), dev, "codes")
     if scales is None:
-        scales = x.new_empty((g, K), dtype=torch.uint8)
+        scales = _new((g, K), torch.uint8, x, stream)
     else:
         _arg(scales, torch.uint8, (g, K), dev, "scales")
     _check(lib.dq_act8_pack(x.data_ptr(), M, K, ld, codes.data_ptr(), scales.data_ptr(), _stream(stream)),
@@ -892,7 +908,7 @@ def dq_act8_unpack(codes, scales, M: int, out=None, stream=None) -> torch.Tensor
     dev = _here(codes, "codes")
     K = _act8_operand(codes, scales, M, dev)
     if out is None:
-        out = codes.new_empty((M, K), dtype=torch.bfloat16)
+        out = _new((M, K), torch.bfloat16, codes, stream)
     else:
         _arg(out, torch.bfloat16, (M, K), dev, "out")
     _check(lib.dq_act8_unpack(codes.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(), _stream(stream)),
@@ -915,12 +931,12 @@ def dq_act8_weight_grad(dy, codes, scales, out=None, out_dtype="bf16", accumulat
     if accumulate and (out is None or oc != DQ_OUT_F32 or bias_grad is True):
         raise ValueError("accumulate needs the fp32 tensors to add to")
     if out is None:
-        out = dy.new_empty((N, K), dtype=odt)
+        out = _new((N, K), odt, dy, stream)
     else:
         _arg(out, odt, (N, K), dev, "out")
     db = None
     if bias_grad is True:
-        db = dy.new_empty((N,), dtype=torch.float32)
+        db = _new((N,), torch.float32, dy, stream)
     elif bias_grad is not False and bias_grad is not None:
         db = bias_grad
         _arg(db, torch.float32, (N,), dev, "bias_grad")
@@ -1024,3 +1040,58 @@ class S24Int8Linear:
                                workspace=self._ws[M], stream=st)
         _used_on(st, self._q, self._s, self._ws[M])
         return y
+
+
+class Act8:
+    """A layer's input kept in 8 bits for the backward pass: blocks of 32 tokens
+    of one feature with a power-of-two scale (dq_act8_pack), half the bytes of
+    bf16.  Any layer here can keep one: weight_grad(dy) gives the gradients of
+    a linear layer's weight and bias, restore() the bf16 values."""
+
+    def __init__(self, codes, scales, M: int):
+        self.codes, self.scales, self.M, self.K = codes, scales, M, scales.shape[1]
+
+    @classmethod
+    def save(cls, x: torch.Tensor, stream=None):
+        return cls(*dq_act8_pack(x, stream=stream), x.shape[0])
+
+    def restore(self, out: torch.Tensor = None, stream=None) -> torch.Tensor:
+        return dq_act8_unpack(self.codes, self.scales, self.M, out=out, stream=stream)
+
+    def weight_grad(self, dy: torch.Tensor, out: torch.Tensor = None, out_dtype="bf16", accumulate: bool = False,
+                    bias_grad=False, stream=None):
+        if dy.shape[0] != self.M:
+            raise ValueError(f"dy: {dy.shape[0]} tokens, the checkpoint holds {self.M}")
+        return dq_act8_weight_grad(dy, self.codes, self.scales, out=out, out_dtype=out_dtype, accumulate=accumulate,
+                                   bias_grad=bias_grad, stream=stream)
+
+
+class Fp4Linear:
+    """The microscaled 4-bit layer: per-block dynamic quantization of bf16
+    activations, then the block-scaled 4-bit product with the dequantization,
+    bias and bf16 rounding fused.  The fp32 weight is quantized once, for
+    training (backward=True) also transposed, with blocks along the output
+    channels: backward_input(dy) is then dy @ W as a 4-bit product like the
+    forward one.  Weight and bias gradients come from an 8-bit checkpoint of
+    the input (Act8.save(x), ckpt.weight_grad(dy)).  Holds no scratch: calls on
+    several streams or in several captured graphs share nothing."""
+
+    def __init__(self, W, sfw, s_col, bias=None, fmt="nv", transposed=None):
+        self.W, self.sfw, self.s_col, self.bias, self.fmt, self.transposed = W, sfw, s_col, bias, fmt, transposed
+        self.N, self.K = W.shape[0], W.shape[1] * 2
+
+    @classmethod
+    def from_float(cls, w: torch.Tensor, bias: torch.Tensor = None, fmt="nv", backward: bool = False):
+        """w: fp32 [N, K], K % 32 == 0, N % 8 == 0 (backward: also N % 32 == 0)."""
+        t = dq_quantize_weight_fp4(w.t().contiguous(), fmt) if backward else None
+        return cls(*dq_quantize_weight_fp4(w, fmt), bias=bias, fmt=fmt, transposed=t)
+
+    def __call__(self, x: torch.Tensor, out: torch.Tensor = None, stream=None):
+        q, sf, s = dq_quantize_rows_fp4(x, self.fmt, stream=stream)
+        return dq_fp4_linear(q, sf, s, self.W, self.sfw, self.s_col, self.bias, fmt=self.fmt, out=out, stream=stream)
+
+    def backward_input(self, dy: torch.Tensor, out: torch.Tensor = None, stream=None):
+        if self.transposed is None:
+            raise ValueError("built without backward=True: no transposed weight")
+        q, sf, s = dq_quantize_rows_fp4(dy, self.fmt, stream=stream)
+        return dq_fp4_linear(q, sf, s, *self.transposed, fmt=self.fmt, out=out, stream=stream)

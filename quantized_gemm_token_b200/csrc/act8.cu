@@ -22,12 +22,12 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "mx.h"
 #include "sm100.cuh"
 
 namespace dq {
 namespace {
 
-constexpr int64_t kAct8MaxDim = int64_t(1) << 30;
 // Single-warp blocks: the blocks tile a row exactly for more row lengths
 // (65792 x 1280, pack: 46.8 us against 50.9 with 128 threads; 2048 x 4096,
 // unpack: 6.2 against 7.9).
@@ -196,12 +196,12 @@ using namespace dq;
 extern "C" {
 
 size_t dq_act8_codes_size(int64_t M, int64_t K) {
-  if (M < 0 || K < 1 || M > kAct8MaxDim || K > kAct8MaxDim) return 0;
+  if (M < 0 || K < 1 || M > kMxMaxDim || K > kMxMaxDim) return 0;
   return static_cast<size_t>((M + 31) / 32 * 32 * K);
 }
 
 size_t dq_act8_scales_size(int64_t M, int64_t K) {
-  if (M < 0 || K < 1 || M > kAct8MaxDim || K > kAct8MaxDim) return 0;
+  if (M < 0 || K < 1 || M > kMxMaxDim || K > kMxMaxDim) return 0;
   return static_cast<size_t>((M + 31) / 32 * K);
 }
 
@@ -209,7 +209,7 @@ dq_status dq_act8_pack(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, in
                        dq_stream_t stream) {
   if (M < 0 || K < 1 || ldx < K) return DQ_ERR_INVALID_ARG;
   if (M > 0 && (x_bf16 == nullptr || codes == nullptr || scales == nullptr)) return DQ_ERR_INVALID_ARG;
-  if (K % 16 != 0 || M > kAct8MaxDim || K > kAct8MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || M > kMxMaxDim || K > kMxMaxDim) return DQ_ERR_UNSUPPORTED;
   if (!aligned(x_bf16, 2) || !aligned(codes, 16) || !aligned(scales, 16)) return DQ_ERR_UNSUPPORTED;
   DeviceInfo* d = nullptr;
   const dq_status st = current_device(&d);
@@ -227,7 +227,7 @@ dq_status dq_act8_unpack(const int8_t* codes, const uint8_t* scales, int64_t M, 
                          dq_stream_t stream) {
   if (M < 0 || K < 1) return DQ_ERR_INVALID_ARG;
   if (M > 0 && (out_bf16 == nullptr || codes == nullptr || scales == nullptr)) return DQ_ERR_INVALID_ARG;
-  if (K % 16 != 0 || M > kAct8MaxDim || K > kAct8MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || M > kMxMaxDim || K > kMxMaxDim) return DQ_ERR_UNSUPPORTED;
   if (!aligned(out_bf16, 16) || !aligned(codes, 16) || !aligned(scales, 16)) return DQ_ERR_UNSUPPORTED;
   DeviceInfo* d = nullptr;
   const dq_status st = current_device(&d);

@@ -38,13 +38,14 @@
 // partial tiles are added through distributed shared memory in split order
 // (no workspace, no atomics).
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 
 #include "gemm_common.cuh"
 #include "internal.h"
+#include "mx.cuh"
+#include "mx.h"
 #include "pipeline.cuh"
 #include "sm100.cuh"
 
@@ -70,7 +71,6 @@ constexpr int WG_OUT_BUF = 2048;             // per epilogue warp: 32 x 32 bf16 
 constexpr int WG_SLOT_COLS = WG_STEP / 2;    // TMEM columns of one converted step
 constexpr int WG_MAX_SMEM = WG_RING * 256 * 64 + WG_EPI_WARPS * WG_OUT_BUF + WG_RING * WG_CODE_STAGE + WG_BAR_BYTES + 1024;
 static_assert(WG_MAX_SMEM <= 227 * 1024, "shared memory");
-constexpr int64_t kGradMaxDim = int64_t(1) << 30;
 
 struct GradArgs {
   int M, N, K;
@@ -731,7 +731,7 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
   if (dw_dtype != DQ_OUT_BF16 && dw_dtype != DQ_OUT_F32) return DQ_ERR_INVALID_ARG;
   if (dw == nullptr || (M > 0 && (dy_bf16 == nullptr || codes == nullptr || scales == nullptr))) return DQ_ERR_INVALID_ARG;
   if (accumulate && dw_dtype != DQ_OUT_F32) return DQ_ERR_INVALID_ARG;
-  if (K % 16 != 0 || N % 8 != 0 || lddy % 8 != 0 || M > kGradMaxDim || N > kGradMaxDim || K > kGradMaxDim ||
+  if (K % 16 != 0 || N % 8 != 0 || lddy % 8 != 0 || M > kMxMaxDim || N > kMxMaxDim || K > kMxMaxDim ||
       lddy > (int64_t(1) << 37))
     return DQ_ERR_UNSUPPORTED;
   if (!aligned(dy_bf16, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(dw, 16) || !aligned(db, 16))

@@ -13,14 +13,14 @@
 // replicated to the four sub-partitions); a tile serves one MMA (NV) or two
 // (MX, selected by the descriptor's scale id).
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 
-#include "fp4.h"
 #include "gemm_common.cuh"
 #include "internal.h"
+#include "mx.cuh"
+#include "mx.h"
 #include "pipeline.cuh"
 #include "sm100.cuh"
 
@@ -769,7 +769,7 @@ dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float* s_row
   if (out_dtype != DQ_OUT_BF16 && out_dtype != DQ_OUT_F32) return DQ_ERR_INVALID_ARG;
   if (W == nullptr || sfw == nullptr || (M > 0 && (A == nullptr || sfa == nullptr || out == nullptr)))
     return DQ_ERR_INVALID_ARG;
-  if (K % 32 != 0 || N % 8 != 0 || M > kFp4MaxDim || N > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (K % 32 != 0 || N % 8 != 0 || M > kMxMaxDim || N > kMxMaxDim || K > kMxMaxDim) return DQ_ERR_UNSUPPORTED;
   if (!aligned(A, 16) || !aligned(sfa, 16) || !aligned(W, 16) || !aligned(sfw, 16) || !aligned(out, 16) ||
       !aligned(s_row, 4) || !aligned(s_col, 16) || !aligned(bias_bf16, 16))
     return DQ_ERR_UNSUPPORTED;

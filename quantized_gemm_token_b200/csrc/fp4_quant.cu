@@ -20,8 +20,8 @@
 // read.  A row stays in registers between the row maximum and the codes.
 #include <cuda_bf16.h>
 
-#include "fp4.h"
 #include "internal.h"
+#include "mx.h"
 #include "sm100.cuh"
 
 namespace dq {
@@ -413,7 +413,7 @@ dq_status quantize_entry(const T* x, int64_t M, int64_t K, int64_t ldx, int fmt,
   const bool nv = fmt == DQ_FP4_NV;
   if ((!nv && fmt != DQ_FP4_MX) || M < 0 || K < 1 || ldx < K || ldq < K / 2) return DQ_ERR_INVALID_ARG;
   if (M > 0 && (x == nullptr || q == nullptr || sf == nullptr || (nv && s == nullptr))) return DQ_ERR_INVALID_ARG;
-  if (K % 32 != 0 || M > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (K % 32 != 0 || M > kMxMaxDim || K > kMxMaxDim) return DQ_ERR_UNSUPPORTED;
   if (!aligned(sf, 16) || !aligned(s, 4) || !aligned(x, sizeof(T))) return DQ_ERR_UNSUPPORTED;
   DeviceInfo* d = nullptr;
   const dq_status st = current_device(&d);
@@ -431,7 +431,7 @@ using namespace dq;
 extern "C" {
 
 size_t dq_fp4_scales_size(int64_t rows, int64_t K, int fmt) {
-  if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || rows < 0 || K < 1 || K % 32 != 0 || rows > kFp4MaxDim || K > kFp4MaxDim)
+  if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || rows < 0 || K < 1 || K % 32 != 0 || rows > kMxMaxDim || K > kMxMaxDim)
     return 0;
   return static_cast<size_t>((rows + 127) / 128 * fp4_atoms(K, fmt) * 512);
 }
@@ -450,7 +450,7 @@ dq_status dq_fp4_dequantize(const uint8_t* q, const uint8_t* sf, const float* s,
                             void* out_bf16, dq_stream_t stream) {
   if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || M < 0 || K < 1) return DQ_ERR_INVALID_ARG;
   if (M > 0 && (q == nullptr || sf == nullptr || out_bf16 == nullptr)) return DQ_ERR_INVALID_ARG;
-  if (K % 32 != 0 || M > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (K % 32 != 0 || M > kMxMaxDim || K > kMxMaxDim) return DQ_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(sf, 16) || !aligned(out_bf16, 16) || !aligned(s, 4)) return DQ_ERR_UNSUPPORTED;
   DeviceInfo* d = nullptr;
   const dq_status st = current_device(&d);
@@ -468,7 +468,7 @@ dq_status dq_fp4_dequantize(const uint8_t* q, const uint8_t* sf, const float* s,
 dq_status dq_fp4_tile_scales(const uint8_t* scales, int64_t rows, int64_t K, int fmt, uint8_t* sf, dq_stream_t stream) {
   if ((fmt != DQ_FP4_MX && fmt != DQ_FP4_NV) || rows < 0 || K < 1) return DQ_ERR_INVALID_ARG;
   if (rows > 0 && (scales == nullptr || sf == nullptr)) return DQ_ERR_INVALID_ARG;
-  if (K % 32 != 0 || rows > kFp4MaxDim || K > kFp4MaxDim) return DQ_ERR_UNSUPPORTED;
+  if (K % 32 != 0 || rows > kMxMaxDim || K > kMxMaxDim) return DQ_ERR_UNSUPPORTED;
   if (!aligned(sf, 16)) return DQ_ERR_UNSUPPORTED;
   DeviceInfo* d = nullptr;
   const dq_status st = current_device(&d);

@@ -169,45 +169,6 @@ dq_status make_tmap_out_2d(CUtensorMap* map, void* base, uint64_t cols, uint64_t
   return DQ_OK;
 }
 
-dq_status make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
-                       uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
-  std::call_once(g_encode_once, resolve_encoder);
-  if (g_encode == nullptr) return cuda_fail(g_encode_err);
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {stride_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  CUtensorMapSwizzle sw = swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                          : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = g_encode(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    t_last_cuda_error = static_cast<int>(r);
-    return DQ_ERR_CUDA;
-  }
-  return DQ_OK;
-}
-
-dq_status make_tmap_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t chunks, uint64_t stride_bytes,
-                           uint32_t box_rows, uint32_t box_chunks) {
-  std::call_once(g_encode_once, resolve_encoder);
-  if (g_encode == nullptr) return cuda_fail(g_encode_err);
-  cuuint64_t dims[3] = {64, rows, chunks};
-  cuuint64_t strides[2] = {stride_bytes, 128};
-  cuuint32_t box[3] = {64, box_rows, box_chunks};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    t_last_cuda_error = static_cast<int>(r);
-    return DQ_ERR_CUDA;
-  }
-  return DQ_OK;
-}
-
 // ------------------------------------------------------------ self test
 
 __global__ void selftest_wait_kernel(WaitCtl ctl) {

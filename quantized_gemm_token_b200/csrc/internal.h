@@ -47,17 +47,6 @@ dq_status make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, ui
                           uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
                           int swizzle_bytes);
 
-// The same for any element type (boxes of up to 256 elements per dimension):
-// swizzle = 128 or 64 (anything else: none).
-dq_status make_tmap_2d(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
-                       uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer, int swizzle_bytes);
-
-// 3-D tensor map over a row-major bf16 matrix as [chunk][row][64 columns], 128B
-// swizzle: one copy of box_rows x box_chunks lays 64-column chunks out one
-// after the other.  `chunks` counts whole chunks of 64 columns only.
-dq_status make_tmap_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint64_t chunks, uint64_t stride_bytes,
-                           uint32_t box_rows, uint32_t box_chunks);
-
 // 2-D tensor map for an output matrix [rows, cols] of 2- or 4-byte elements
 // (row stride in bytes), box {32 cols, 32 rows}, swizzle matching a 32-column
 // row: 64 B (2-byte elements) or 128 B (4-byte elements).

@@ -90,47 +90,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
   }
 }
 
-// One lane of a converged warp (the same one every time).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
-// Whether the phase with the given parity of `bar` has completed (no waiting).
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// mbar_wait by a whole converged warp; the result is the warp's.  An issuing
-// warp that stays converged (this wait, and elect_one() around the
-// instructions that one thread issues) keeps its descriptors and addresses in
-// uniform registers, where tcgen05 instructions take them from; in a branch of
-// a single lane each of them costs register moves of some 60 - 100 cycles.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
-                                               volatile int* abort) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, ctl, abort));
-}
-
-// The same for two phases that were tested (mbar_test) earlier: a test's answer takes about 100 cycles, so a loop that feeds the
-// tensor core asks for the next step's before it issues the present one's
-// MMAs (two waits and two commits per 512-cycle step: 661 cycles per step
-// without, 515 with).
-__device__ __forceinline__ bool mbar_wait_warp2(bool tested, uint32_t bar0, uint32_t parity0, uint32_t bar1,
-                                                uint32_t parity1, const WaitCtl& ctl, volatile int* abort) {
-  if (__all_sync(0xffffffffu, tested)) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar0, parity0, ctl, abort) && mbar_wait(bar1, parity1, ctl, abort));
-}
-
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
