@@ -85,6 +85,7 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, ui
 //   accumulator, all six write the output.
 constexpr int FS_THREADS = 192;
 constexpr int FS_MAX_STAGES = 8;
+constexpr int FS_PREFETCH = 4;
 constexpr int FS_BAR_BYTES = 256;
 
 struct FewArgs {
@@ -152,13 +153,22 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   griddep_launch_dependents();
-  griddep_wait();
 
   // unit: (channel tile, split), splits neighbouring (one cluster)
   const int nt = blockIdx.x / g.splits;
   const int split = blockIdx.x - nt * g.splits;
   const int kb0 = static_cast<int>(static_cast<int64_t>(split) * g.kb_total / g.splits);
   const int kb1 = static_cast<int>(static_cast<int64_t>(split + 1) * g.kb_total / g.splits);
+
+  // while the kernel before this one (which quantizes the tokens) still runs,
+  // the first stages' weights come to L2
+  if (warp == 0 && elect_one())
+    for (int kb = kb0; kb < min(kb1, kb0 + FS_PREFETCH); ++kb) {
+      tma_prefetch_2d(&tm_w, kb * F4_KB, nt * 128);
+      tma_prefetch_2d(&tm_sw, kb * T * 64, nt);
+    }
+  __syncwarp();
+  griddep_wait();
 
   if (warp == 0) {
     int stage = 0;

@@ -388,18 +388,19 @@ dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, in
   const int64_t rows = (M + 127) / 128 * 128;
   const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
   if constexpr (sizeof(T) == 2) {
-    if (K <= 16384 && ldx % 8 == 0 && aligned(x, 16) && ldq % 8 == 0 && aligned(q, 8)) {
-      // two runs per thread where 256 threads hold the row so, else four
+    if (K <= 32768 && ldx % 8 == 0 && aligned(x, 16) && ldq % 8 == 0 && aligned(q, 8)) {
+      // two runs per thread where 256 threads hold the row so, else four or eight
       const int64_t nu = K / 16;
       int vpt = nu <= 32 ? 1 : 2;
       int lg = 5;
       while (lg < 8 && (static_cast<int64_t>(vpt) << lg) < nu) ++lg;
-      if ((static_cast<int64_t>(vpt) << lg) < nu) vpt = 4;
+      while ((static_cast<int64_t>(vpt) << lg) < nu) vpt *= 2;
       const int64_t blocks = (rows + (256 >> lg) - 1) / (256 >> lg);
       const bool wide = aligned(x, 32) && ldx % 16 == 0;
       auto k = vpt == 1   ? (wide ? fp4_rows_kernel<NV, 1, true> : fp4_rows_kernel<NV, 1, false>)
                : vpt == 2 ? (wide ? fp4_rows_kernel<NV, 2, true> : fp4_rows_kernel<NV, 2, false>)
-                          : (wide ? fp4_rows_kernel<NV, 4, true> : fp4_rows_kernel<NV, 4, false>);
+               : vpt == 4 ? (wide ? fp4_rows_kernel<NV, 4, true> : fp4_rows_kernel<NV, 4, false>)
+                          : (wide ? fp4_rows_kernel<NV, 8, true> : fp4_rows_kernel<NV, 8, false>);
       return launch(k, blocks, stream, x, M, K, ldx, q, ldq, sf, atoms, s_row, lg);
     }
   }

@@ -51,6 +51,15 @@ __device__ __forceinline__ bool mbar_wait_warp2(bool tested, uint32_t bar0, uint
   return __all_sync(0xffffffffu, mbar_wait(bar0, parity0, ctl, abort) && mbar_wait(bar1, parity1, ctl, abort));
 }
 
+// Brings a tile towards L2 only: no shared memory, nothing to wait for.  L2 is
+// where all writers of the tile meet, so unlike a load it may be issued before
+// the kernels ahead in the stream have completed.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 namespace pipe {
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {

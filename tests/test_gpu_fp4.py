@@ -63,7 +63,7 @@ def _check_quantized(x, fmt, q, sf, s):
     return codes, E, sr
 
 
-SHAPES = [(1, 32), (1, 64), (3, 96), (5, 480), (33, 160), (130, 1280), (129, 4096), (40, 8192), (3, 16384), (2, 16416)]
+SHAPES = [(1, 32), (1, 64), (3, 96), (5, 480), (33, 160), (130, 1280), (129, 4096), (40, 8192), (3, 16384), (2, 16416), (2, 28672), (1, 32768), (1, 32800)]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
