@@ -34,9 +34,15 @@
 // db: in the tiles of the first 256 features the epilogue warps also add up
 // the dY tile that lies in shared memory (each lane eight channels), so dY is
 // not read again: there a stage's MMAs hand it to them, and they free it.
-// Few tiles: the tokens are split over a cluster of up to 4 pairs whose fp32
-// partial tiles are added through distributed shared memory in split order
-// (no workspace, no atomics).
+// A partial wave of tiles: their tokens are split over a cluster of 2 or 4
+// pairs whose fp32 partial tiles are added through distributed shared memory in
+// split order (no workspace, no atomics), in a second launch where whole waves
+// come first.
+// Measured (bound: the MMAs' 512 cycles per step, about 590 reached): 8192 x
+// 4096 x 4096 197 us, 1393 TFLOP/s (0.82 of the measured bf16 burst, 0.97 of
+// the sustained rate); 65792 tokens, 1280 -> 5120, fp32: 619 us, 696 us with db
+// (dY read again by a kernel of its own: 790 - 870 us); 2048 x 4096 x 4096 54 us
+// (256 tiles on 74 pairs, the fourth wave 34).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -704,6 +710,11 @@ dq_status grad_clusters(const DeviceInfo& d, int splits, int* out) {
   std::atomic<int>& slot = g_grad_clusters[d.device & 63][splits == 1 ? 0 : splits == 2 ? 1 : 2];
   int n = slot.load(std::memory_order_relaxed);
   if (n == 0) {
+    // the register split must fit what the block is launched with
+    cudaFuncAttributes fa;
+    cudaError_t fe = cudaFuncGetAttributes(&fa, act8_grad_kernel);
+    if (fe != cudaSuccess) return cuda_fail(fe);
+    if (fa.numRegs < WG_REGS) return DQ_ERR_UNSUPPORTED;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = grad_config(attr, splits, WG_MAX_SMEM, nullptr);
     cfg.numAttrs = 1;                                     // the cluster shape only

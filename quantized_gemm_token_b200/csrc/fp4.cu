@@ -77,10 +77,12 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, ui
 // ---------------------------------------------------------------- few tokens
 // The weight stream is the bound (0.53 - 0.56 bytes per weight at HBM rate),
 // so the weight's 128 channels sit on the MMA's M and the tokens on its N, one
-// work unit per CTA, several CTAs per SM: their loads overlap each other's
+// work unit per CTA, two CTAs per SM: their loads overlap each other's
 // prologue, pipeline ends and epilogue.  Few channel tiles: the features are
 // split over a cluster of up to 8 CTAs, whose fp32 partial tiles are added
-// through distributed shared memory in split order.
+// through distributed shared memory in split order.  Measured, K = 8192, N =
+// 28672: 24.2 us at one token (NV, 132 MB, 5.47 TB/s, 0.85 of the measured copy
+// rate), 23.8 us at 16 (MX).
 //   warp 0 producer, warp 1 scale copies and MMAs, warps 2..5 drain the
 //   accumulator, all six write the output.
 constexpr int FS_THREADS = 192;
@@ -313,13 +315,20 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- many tokens
-// A pair of SMs per 256 x 256 (or narrower) tile (cta_group::2), as the int8 pair kernel:
-// each CTA loads its 128 token rows and half of the tile's weight rows, plus
-// its own rows' scale tiles and ALL of the tile's weight scale tiles (each
-// SM's tensor core multiplies its rows with every column, so both tensor
+// A pair of SMs per 256 x 256 (or narrower) tile (cta_group::2), as the int8
+// pair kernel: each CTA loads its 128 token rows and half of the tile's weight
+// rows, plus its own rows' scale tiles and ALL of the tile's weight scale tiles
+// (each SM's tensor core multiplies its rows with every column, so both tensor
 // memories need every column's scales).
 //   warp 0 producer, warp 1 (leader) scale copies and MMAs, warps 2..9
 //   epilogue, two per TMEM sub-partition on alternate 32-column chunks.
+// What bounds it: a 256-feature stage is 512 cycles of MMAs, and a CTA loads
+// 38.9 KB for it (NV), 608 cycles at the 64 bytes per cycle an SM takes from L2;
+// measured 660 - 680.  Narrower tiles load more per MMA (192 columns: 34.8 KB
+// for 384 cycles).  Measured: 8192^3 196 us (NV, 5.62 PFLOP/s, 0.83 of four
+// times the measured bf16 rate), 184 us (MX); 2048 x 4096 x 4096 19.0 us, of
+// which 5.7 us are launch, prologue and the pipeline's ends and 3.4 us the
+// last tiles' epilogue (16.8 MB of output).
 template <bool NV>
 struct CfgP {
   static constexpr int BN = 256;
@@ -566,19 +575,23 @@ __global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
       const int n0 = geo.n0, nch = geo.width / 32;
       const int m_slab = geo.ta * 256 + static_cast<int>(rank) * 128 + sp * 32;
       const int m = m_slab + lane;
+      bool free_slot = true;
       if (ep_tid == 0) {
-        if (t != pair && !mbar_wait(smem_u32(sc_free), sc_phase ^ 1, g.wait, abort_flag)) break;
-        // the tile's column scales (unless there are none) and bias
-        const int ncols = min(geo.width, g.N - n0);
-        const uint32_t sb = !g.out_s32 && g.s_col != nullptr && ncols > 0 ? static_cast<uint32_t>(ncols) * 4u : 0u;
-        const uint32_t bb = !g.out_s32 && g.bias != nullptr && ncols > 0 ? static_cast<uint32_t>(ncols) * 2u : 0u;
-        mbar_arrive_expect_tx(smem_u32(sc_full), sb + bb);
-        if (sb) bulk_load_1d(sc_slot, g.s_col + n0, sb, smem_u32(sc_full));
-        if (bb) bulk_load_1d(sc_slot + kScBiasOff, g.bias + n0, bb, smem_u32(sc_full));
+        free_slot = t == pair || mbar_wait(smem_u32(sc_free), sc_phase ^ 1, g.wait, abort_flag);
+        if (free_slot) {
+          // the tile's column scales (unless there are none) and bias
+          const int ncols = min(geo.width, g.N - n0);
+          const uint32_t sb = !g.out_s32 && g.s_col != nullptr ? static_cast<uint32_t>(ncols) * 4u : 0u;
+          const uint32_t bb = !g.out_s32 && g.bias != nullptr ? static_cast<uint32_t>(ncols) * 2u : 0u;
+          mbar_arrive_expect_tx(smem_u32(sc_full), sb + bb);
+          if (sb) bulk_load_1d(sc_slot, g.s_col + n0, sb, smem_u32(sc_full));
+          if (bb) bulk_load_1d(sc_slot + kScBiasOff, g.bias + n0, bb, smem_u32(sc_full));
+        }
       }
+      if (!__all_sync(0xffffffffu, free_slot)) break;    // (a warp leaves whole)
       const float srow = (!g.out_s32 && g.s_row != nullptr && m < g.M) ? __ldg(g.s_row + m) : 1.0f;
-      if (!mbar_wait(smem_u32(accf_bar), acc_phase, g.wait, abort_flag)) break;
-      if (!mbar_wait(smem_u32(sc_full), sc_phase, g.wait, abort_flag)) break;
+      if (!mbar_wait_warp(smem_u32(accf_bar), acc_phase, g.wait, abort_flag)) break;
+      if (!mbar_wait_warp(smem_u32(sc_full), sc_phase, g.wait, abort_flag)) break;
       acc_phase ^= 1;
       sc_phase ^= 1;
       tc_fence_after();
