@@ -418,7 +418,7 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
  *     with an e4m3 scale d = e4m3(fp32((a / s) / 6)); code = e2m1(x / (d s))
  *     decided on the exact quotient, 0 where d = 0; the value is e2m1 * d * s.
  * Codes, block scales and row scales are bit-equal to a scalar evaluation of
- * these definitions.  A block (MX) or row (NV) with a NaN or an infinity gets
+ * these definitions, but for the sign of a zero code, which is free.  A block (MX) or row (NV) with a NaN or an infinity gets
  * a NaN scale (E = 255; s = NaN, its block scales and codes 0), so every
  * product computed from it is NaN.
  *
@@ -426,8 +426,9 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
  * tile (row block, block group) row-major: byte 16 (r % 32) + 4 ((r % 128) /
  * 32) + b % 4 of tile (r / 128, b / 4).  dq_fp4_scales_size() is the buffer's
  * size; dq_fp4_tile_scales converts the plain [rows, K / block] form.  Bytes
- * past the last row or block of a tile are written as 0; bytes past the last
- * BLOCK must be finite scales when a caller fills the buffer itself.
+ * past the last row or block of a tile are written as 0.  A caller that fills
+ * the buffer itself writes finite scales past the last BLOCK, and e4m3 scales
+ * without a sign.
  *
  * dq_quantize_rows_fp4: x bf16 [M, K] (row stride ldx) -> q [M, K/2] (row
  *   stride ldq bytes), sf, s_row fp32 [M] (NV; ignored for MX, may be NULL).
@@ -435,7 +436,8 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
  *   K <= 32768 take the single-pass kernel, others a slower one.
  * dq_quantize_weight_fp4: the same for fp32 rows (output channels).
  * dq_fp4_dequantize: out bf16 [M, K] = bf16(fp32(e2m1 * d) * s); s may be
- *   NULL (1).  Exact for what the quantizers write.
+ *   NULL (1).  Exact for what the quantizers write (an NV value above bf16's
+ *   largest, from a row that reaches it, becomes an infinity).
  * dq_fp4_linear: acc[m, n] = sum over blocks of sfa sfw sum a w on the tensor
  *   cores (tcgen05.mma kind::mxf4nvf4.block_scale, fp32 accumulators);
  *   DQ_OUT_BF16: out = bf16(((acc * s_row[m]) * s_col[n]) + bias[n]), each op

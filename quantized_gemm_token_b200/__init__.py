@@ -810,8 +810,8 @@ def dq_fp4_tile_scales(scales: torch.Tensor, fmt="nv", sf: torch.Tensor = None, 
 
 def _fp4_operand(q, sf, s, code: int, dev: int, name: str):
     """(rows, K) of a 4-bit operand with its tiled block scales and row scales."""
-    if q.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dims, got {q.dim()}")
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError(f"{name}: expected a tensor of 2 dims")
     _arg(q, torch.uint8, q.shape, dev, name)
     R, K = q.shape
     K *= 2

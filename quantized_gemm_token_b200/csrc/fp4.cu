@@ -15,7 +15,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -676,7 +675,7 @@ dq_status launch_few(const uint8_t* A, const uint8_t* sfa, int64_t M, int64_t K,
   if ((st = make_tmap_sf(&tsw, sfw, (N + 127) / 128, atoms, T, 1)) != DQ_OK) return st;
   if ((st = make_tmap_sf(&tsx, sfa, (M + 127) / 128, atoms, T, 1)) != DQ_OK) return st;
   auto k = fp4_few_kernel<NV>;
-  if ((st = smem_limit_once(reinterpret_cast<const void*>(k), smem)) != DQ_OK) return st;
+  if ((st = smem_limit_once(reinterpret_cast<const void*>(k), limit)) != DQ_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(g.nt * g.splits));
   cfg.blockDim = dim3(FS_THREADS);

@@ -30,7 +30,7 @@ namespace dq {
 namespace {
 
 // Eight fp32 values -> eight e2m1 codes (value 2i in the low nibble of byte
-// i), nearest with ties to even, saturating; -0 keeps its sign.
+// i), nearest with ties to even, saturating.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
   uint32_t r;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
