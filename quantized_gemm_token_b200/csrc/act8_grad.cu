@@ -34,15 +34,16 @@
 // db: in the tiles of the first 256 features the epilogue warps also add up
 // the dY tile that lies in shared memory (each lane eight channels), so dY is
 // not read again: there a stage's MMAs hand it to them, and they free it.
-// A partial wave of tiles: their tokens are split over a cluster of 2 or 4
-// pairs whose fp32 partial tiles are added through distributed shared memory in
-// split order (no workspace, no atomics), in a second launch where whole waves
-// come first.
+// A partial wave of tiles: they are halved (128 channels) where the halves fit
+// in one wave (2048 x 2560 x 2048, 80 tiles on 74 pairs: 26.8 us, whole 29.1), or
+// their tokens are split over a cluster of 2 or 4 pairs whose fp32 partial
+// tiles are added through distributed shared memory in split order (no
+// workspace, no atomics), in a second launch where whole waves come first.
 // Measured (bound: the MMAs' 512 cycles per step, about 590 reached): 8192 x
 // 4096 x 4096 197 us, 1393 TFLOP/s (0.82 of the measured bf16 burst, 0.97 of
 // the sustained rate); 65792 tokens, 1280 -> 5120, fp32: 619 us, 696 us with db
-// (dY read again by a kernel of its own: 790 - 870 us); 2048 x 4096 x 4096 54 us
-// (256 tiles on 74 pairs, the fourth wave 34).
+// (dY read again by a kernel of its own: 790 - 870 us); 2048 x 4096 x 4096 53.5 us
+// (256 tiles on 74 pairs; 5 us of it are launch, prologue and ends).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -82,6 +83,7 @@ struct GradArgs {
   int M, N, K;
   int bn;                  // channels per tile (128 or 256), half of them per CTA
   int kt, nt;              // feature tiles (256), channel tiles
+  int t1;                  // tiles from here on are halved (128 channels each)
   int tile0;               // first tile of this launch
   int splits, units;
   int ks;                  // token steps: ceil(M / 64)
@@ -198,21 +200,29 @@ __device__ __forceinline__ void codes4_top(uint32_t w, uint32_t e, uint32_t& r0,
 }
 
 struct GradUnit {
-  int split, kt, nt, s0, s1;
+  int split, kt, n0, bn, s0, s1;
 };
 __device__ __forceinline__ GradUnit grad_unit(const GradArgs& g, int u) {
   GradUnit t;
   int tile = u / g.splits;
   t.split = u - tile * g.splits;
   tile += g.tile0;
+  t.bn = g.bn;
+  t.n0 = 0;
+  if (tile >= g.t1) {
+    t.bn = 128;
+    t.n0 = ((tile - g.t1) & 1) * 128;
+    tile = g.t1 + ((tile - g.t1) >> 1);
+  }
   if (g.db != nullptr) {
     // the tiles that also sum columns (kt = 0, the slowest) come last, where a
     // partial wave is split
     t.kt = g.kt - 1 - tile / g.nt;
-    t.nt = tile % g.nt;
+    t.n0 += tile % g.nt * g.bn;
   } else {
-    t.nt = tile / g.kt;
-    t.kt = tile - t.nt * g.kt;
+    const int nt = tile / g.kt;
+    t.kt = tile - nt * g.kt;
+    t.n0 += nt * g.bn;
   }
   t.s0 = static_cast<int>(static_cast<int64_t>(t.split) * g.ks / g.splits);
   t.s1 = static_cast<int>(static_cast<int64_t>(t.split + 1) * g.ks / g.splits);
@@ -228,8 +238,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const smem = smem_raw + (base - raw);
   // rings: this CTA's half of dY (bn / 128 chunks of 64 tokens x 128 B); codes, then their scales [2][128]
-  const int half_n = g.bn / 2;
-  const uint32_t y_bytes = static_cast<uint32_t>(half_n) * 128u;
+  const uint32_t y_bytes = static_cast<uint32_t>(g.bn) * 64u;
   uint64_t* const yfull = reinterpret_cast<uint64_t*>(smem + g.off_bar);   // leader: both halves of dY
   uint64_t* const yempty = yfull + WG_RING;
   uint64_t* const qfull = yempty + WG_RING;
@@ -293,13 +302,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       uint32_t phase = 0;
       long long issued = 0;
       bool ok = true;
-      const int chunks = half_n / 64;
       for (int u = u0; ok && u < g.units; u += G) {
         const GradUnit t = grad_unit(g, u);
-        const int c0 = t.nt * 2 * chunks + static_cast<int>(rank) * chunks;
+        const int chunks = t.bn / 128;
+        const int c0 = t.n0 / 64 + static_cast<int>(rank) * chunks;
         const int f0 = t.kt * 256 + static_cast<int>(rank) * 128;
-        // the 3-D map covers whole chunks only: a tile that holds the ragged last one is loaded chunk by chunk
-        const bool whole = c0 + chunks <= g.full_chunks || g.N % 64 == 0;
+        // the 3-D map covers whole chunks only, a whole tile's at a time: a tile that holds the ragged last one and
+        // a halved tile are loaded chunk by chunk
+        const bool whole = t.bn == g.bn && (c0 + chunks <= g.full_chunks || g.N % 64 == 0);
         for (int s = t.s0; s < t.s1; ++s) {
           if (!mbar_wait_warp(smem_u32(empty + stage), phase ^ 1, g.wait, abort_flag)) {
             ok = false;
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
               tma_load_2d(sq, &tm_q, fb, f0 * 2, s * 4);
               tma_load_2d(sq + WG_CODES, &tm_e, fb, f0, s * 2);
             } else {
-              if (rank == 0) mbar_arrive_expect_tx(fb, 2u * y_bytes);
+              if (rank == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(t.bn) * 128u);
               const uint32_t fl = map_to_rank(fb, lead);
               if (whole)
                 tma_load_3d_pair(sy, &tm_y3, fl, 0, s * WG_STEP, c0);
@@ -349,12 +359,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       }
     } else if (warp == 1 && rank == 0) {
       // -------------------------------------------------------- MMA issuer
-      const uint32_t idesc = idesc_grad(g.bn);
       int stage = 0;
       uint32_t phase = 0, aphase = 0;
       bool ok = true, tested = false;             // tested: the next step's operands were found ready
       for (int u = u0; ok && u < g.units; u += G) {
         const GradUnit t = grad_unit(g, u);
+        const uint32_t idesc = idesc_grad(t.bn);
         // a stage is freed by the MMAs, or in db tiles by the two warps that sum it
         uint64_t* const ynext = g.db != nullptr && t.kt == 0 ? ydone : yempty;
         const bool twice = g.db != nullptr && t.kt != 0;
@@ -463,16 +473,17 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     set_regs_up<WG_REGS_EPI>();
     const int ew = warp - WG_EPI_WARP0;
     const int q = warp & 3;
-    const int half = g.bn / 2;                   // channels of this warp: [h0, h0 + half) of the tile
-    const int h0 = (ew >> 2) * half;
     const uint32_t buf = base + g.off_out + static_cast<uint32_t>(ew) * WG_OUT_BUF;
-    const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h0);
     int stage = 0;
     uint32_t aphase = 0;
     uint32_t dphase = 0;                         // bit s: the phase of ydone[s], which only db tiles use
     bool ok = true;
     for (int u = u0; ok && u < g.units; u += G) {
       const GradUnit t = grad_unit(g, u);
+      const int half_n = t.bn / 2;                 // channels of this CTA's half of dY, and of
+      const int half = half_n;                     // this warp: [h0, h0 + half) of the tile
+      const int h0 = (ew >> 2) * half;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h0);
       float sum[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
@@ -543,7 +554,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
         break;
       }
       const int k0 = t.kt * 256 + static_cast<int>(rank) * 128 + q * 32;
-      const int n0 = t.nt * g.bn + h0;
+      const int n0 = t.n0 + h0;
       if (with_db) {
         // the lanes of a unit, then the eight warps in order; the sums of this CTA's channels go to db, or for
         // a split beside the partial tile
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             v += __uint_as_float(pipe::lds32(base + g.off_out + static_cast<uint32_t>(w * WG_OUT_BUF + c * 4)));
         named_bar_sync(1, 32 * WG_EPI_WARPS);              // read before the buffers are used again
         if (c < half_n) {
-          const int n = t.nt * g.bn + static_cast<int>(rank) * half_n + c;
+          const int n = t.n0 + static_cast<int>(rank) * half_n + c;
           if (g.splits > 1) pipe::sts32(base + g.off_out + static_cast<uint32_t>(c) * 4u, __float_as_uint(v));
           else if (n < g.N) g.db[n] = g.accumulate ? g.db[n] + v : v;
         }
@@ -639,7 +650,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
     for (int i = threadIdx.x; i < (r1 - r0) * 32; i += WG_THREADS) {
       const int ch = r0 + (i >> 5);
       const int quad = i & 31;
-      const int n = t.nt * g.bn + ch;
+      const int n = t.n0 + ch;
       const int k = t.kt * 256 + static_cast<int>(rank) * 128 + 4 * quad;
       if (n >= g.N || k >= g.K) continue;              // K % 16 == 0: the quad is all in or all out
       const uint32_t off = base + static_cast<uint32_t>(ch * 128 + 4 * quad) * 4u;
@@ -664,8 +675,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
             make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
       }
     }
-    if (g.db != nullptr && t.kt == 0 && t.split == 0 && static_cast<int>(threadIdx.x) < half_n / 4) {
-      const int n = t.nt * g.bn + static_cast<int>(rank) * half_n + 4 * static_cast<int>(threadIdx.x);
+    if (g.db != nullptr && t.kt == 0 && t.split == 0 && static_cast<int>(threadIdx.x) < g.bn / 8) {
+      const int n = t.n0 + static_cast<int>(rank) * (g.bn / 2) + 4 * static_cast<int>(threadIdx.x);
       if (n < g.N) {                                   // N % 8 == 0
         const uint32_t off = base + g.off_out + threadIdx.x * 16u;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -771,29 +782,36 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
   for (int i = 0; i < 3; ++i)
     if ((st = grad_clusters(*dev, 1 << i, fit + i)) != DQ_OK) return st;
   const int pairs = fit[0];
-  // Tile width with the least estimated time, in steps: whole waves of tiles,
-  // then the remaining tiles with their tokens split over 2 or 4 pairs where
-  // that still fits in one wave (a launch of its own).
+  // The plan with the least estimated time: whole waves of tiles, then the
+  // remaining ones as they are, halved (128 channels), or with their tokens
+  // split over 2 or 4 pairs (a launch of its own), where that still fits in one
+  // wave.
   int64_t tiles = 0;
   int rest = 0, rest_splits = 1;
+  bool halved = false;
   double best = 1e300;
   for (int bn = 128; bn <= 256; bn += 128) {
     const int64_t nt = (N + bn - 1) / bn, n = nt * g.kt;
     const double step = bn == 256 ? 0.31 : 0.24, ends = 4.0;       // us
     const int64_t waves = n / pairs, r = n % pairs;
+    auto take = [&](double cost, int sp, bool hv) {
+      if (cost >= 0.98 * best) return;
+      best = cost;
+      g.bn = bn;
+      g.nt = static_cast<int>(nt);
+      tiles = n;
+      rest = sp > 1 || hv ? static_cast<int>(r) : 0;
+      rest_splits = sp;
+      halved = hv;
+    };
+    if (bn == 256 && waves > 0 && r > 0 && 2 * r <= pairs)
+      take(static_cast<double>(waves) * (g.ks * step + ends) + g.ks * 0.24 + ends, 1, true);
     for (int sp = 1; sp <= 4; sp *= 2) {
       if (sp > 1 && (r == 0 || r > fit[sp / 2] || g.ks < 4 * sp)) break;
       const double cost = static_cast<double>(waves) * (g.ks * step + ends) +
                           (r > 0 ? (g.ks + sp - 1) / sp * step + ends : 0.0) +
                           (sp > 1 ? (waves > 0 ? 10.0 : 5.0) : 0.0);   // the join, and a second launch
-      if (cost < 0.98 * best) {
-        best = cost;
-        g.bn = bn;
-        g.nt = static_cast<int>(nt);
-        tiles = n;
-        rest = sp > 1 ? static_cast<int>(r) : 0;
-        rest_splits = sp;
-      }
+      take(cost, sp, false);
     }
   }
   if (tiles > 0x1fffffff) return DQ_ERR_UNSUPPORTED;
@@ -846,6 +864,9 @@ dq_status dq_act8_weight_grad(const void* dy_bf16, int64_t M, int64_t N, int64_t
     return e == cudaSuccess ? DQ_OK : cuda_fail(e);
   };
   const int whole = static_cast<int>(tiles) - rest;
+  g.t1 = whole;
+  if (halved) return run(0, whole + 2 * rest, 1);
+  g.t1 = static_cast<int>(tiles);
   if (whole > 0 && (st = run(0, whole, 1)) != DQ_OK) return st;
   return rest > 0 ? run(whole, rest, rest_splits) : DQ_OK;
 }

@@ -105,6 +105,24 @@ def test_many_tokens_full_grid():
     _check(*dq.dq_act8_weight_grad(dy, codes, scales, out_dtype="f32", bias_grad=True), dy, x)
 
 
+@pytest.mark.parametrize("out,accumulate", [("bf16", False), ("f32", False), ("f32", True)])
+@pytest.mark.parametrize("M,N,K", [(130, 2312, 2064), (2048, 2560, 2048), (1601, 2184, 2320)])
+def test_more_tiles_than_one_wave(M, N, K, out, accumulate):
+    """81 to 90 tiles of 256 x 256: the ones past the first wave are halved (with
+    a half that lies outside the matrix, and ragged ones) or split."""
+    dy, codes, scales, x = _case(M, N, K, 4)
+    if accumulate:
+        base, dbase = torch.ones((N, K), device="cuda"), torch.ones((N,), device="cuda")
+        dw, db = dq.dq_act8_weight_grad(dy, codes, scales, out=base.clone(), out_dtype=out, accumulate=True,
+                                        bias_grad=dbase.clone())
+        _check(dw, db, dy, x, base.double(), dbase.double())
+    else:
+        dw, db = dq.dq_act8_weight_grad(dy, codes, scales, out_dtype=out, bias_grad=True)
+        _check(dw, db, dy, x)
+        again, _ = dq.dq_act8_weight_grad(dy, codes, scales, out_dtype=out)
+        assert torch.equal(again, dw)
+
+
 def test_against_differences():
     """dW and db of L = sum (x W^T + b - t)^2 / 2 against central differences of
     L in 64 bits (exact for a quadratic but for rounding); dY is rounded to bf16
