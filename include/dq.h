@@ -1,7 +1,8 @@
 /*
  * dq.h -- C ABI of libdq: the int8 dynamic-quantization linear layer on
  * NVIDIA B200 (sm_100a), dense and block-sparse (BSR) weight, with its
- * dynamic FP8 sibling and the weight-only int4 (HQQ) linear.
+ * dynamic FP8 and microscaled 4-bit siblings, the weight-only int4 (HQQ)
+ * linear, and 8-bit activation checkpoints with the weight gradient from them.
  *
  * The layer (pytorch/ao PR 821, "int8 dynamic quant + bsr support",
  * description and review) is
