@@ -479,7 +479,7 @@ DQ_API dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float
  * code 0.
  *
  * dq_act8_pack: x bf16 [M, K] (row stride ldx, any 2-byte aligned address;
- *   8-byte aligned rows take wide loads) -> codes, scales.
+ *   8- and 16-byte aligned rows take wide loads) -> codes, scales.
  * dq_act8_unpack: codes, scales -> out bf16 [M, K] contiguous.
  * dq_act8_weight_grad: the gradients of out = x W^T + bias from dY bf16 [M, N]
  *   (row stride lddy) and the checkpoint of x:

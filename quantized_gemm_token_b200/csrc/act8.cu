@@ -29,8 +29,7 @@ namespace dq {
 namespace {
 
 // Single-warp blocks: the blocks tile a row exactly for more row lengths
-// (65792 x 1280, pack: 46.8 us against 50.9 with 128 threads; 2048 x 4096,
-// unpack: 6.2 against 7.9).
+// (2048 x 4096, unpack: 6.2 us against 7.9 with 128 threads).
 constexpr int ACT8_THREADS = 32;
 
 // 2^(E - 133) as bf16 bits, NaN for E = 255.
@@ -39,83 +38,104 @@ __device__ __forceinline__ uint32_t act8_scale_bf16(uint32_t e) {
   return e >= 7u ? (e - 6u) << 7 : 1u << e;
 }
 
-// HBM bound: 2 bytes read, 33/32 written per element (65792 x 1280: 46.8 us,
-// 5.45 TB/s, 0.84 of the copy rate).  A thread holds 4
-// features x 32 tokens (32 loads of 8 bytes, a warp covering 256 contiguous
-// bytes of a row), so the block maximum never leaves its registers, and
-// writes each half block of its features as 64 contiguous bytes.
-// VEC: 8-byte aligned rows; else element loads.
-template <bool VEC>
-__global__ void __launch_bounds__(ACT8_THREADS) act8_pack_kernel(const uint16_t* __restrict__ x, int64_t M, int K, int64_t ldx,
-                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+// HBM bound: 2 bytes read, 33/32 written per element (65792 x 1280: 41.0 us,
+// 6.22 TB/s, 0.96 of the copy rate).  Lane l holds 8 features x 16 tokens (half l
+// / 16 of the block: 16 loads of 16 bytes, half a warp covering 256 contiguous
+// bytes of a row); the halves' maxima meet in one exchange, and a lane writes
+// its half block as 128 contiguous bytes, 32 at a time: whole sectors
+// (with 16-byte stores 49.0 us; 4 features x 32 tokens per lane 46.7).
+// LOAD: bytes per load, 16 or 8 by the rows' alignment, else 2; WIDE: 32-byte
+// aligned codes (as an argument instead: 43.1 us).
+template <int LOAD, bool WIDE>
+__global__ void __launch_bounds__(ACT8_THREADS) act8_pack_kernel(const uint16_t* __restrict__ x, int64_t M, int K,
+                                                                 int64_t ldx, uint8_t* __restrict__ codes,
+                                                                 uint8_t* __restrict__ scales) {
   griddep_launch_dependents();
   griddep_wait();
-  const int k = (blockIdx.x * ACT8_THREADS + threadIdx.x) * 4;
-  if (k >= K) return;
+  const int h = threadIdx.x >> 4;
+  const int k = blockIdx.x * 128 + (threadIdx.x & 15) * 8;
+  const bool in = k < K;
   for (int64_t blk = blockIdx.y; blk * 32 < M; blk += gridDim.y) {
-    const int64_t m0 = blk * 32;
-    uint2 v[32];
-    uint32_t lo = 0, hi = 0;               // largest magnitudes of features (0, 1) and (2, 3)
+    const int64_t m0 = blk * 32 + 16 * h;
+    uint4 v[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      v[j] = make_uint2(0u, 0u);
-      if (m0 + j < M) {
+    for (int j = 0; j < 16; ++j) {
+      v[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (in && m0 + j < M) {
         const uint16_t* p = x + (m0 + j) * ldx + k;
-        if (VEC) {
-          v[j] = __ldcs(reinterpret_cast<const uint2*>(p));
+        if (LOAD == 16) {
+          v[j] = __ldcs(reinterpret_cast<const uint4*>(p));
+        } else if (LOAD == 8) {
+          const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p)), b = __ldcs(reinterpret_cast<const uint2*>(p) + 1);
+          v[j] = make_uint4(a.x, a.y, b.x, b.y);
         } else {
           v[j].x = static_cast<uint32_t>(p[0]) | (static_cast<uint32_t>(p[1]) << 16);
           v[j].y = static_cast<uint32_t>(p[2]) | (static_cast<uint32_t>(p[3]) << 16);
+          v[j].z = static_cast<uint32_t>(p[4]) | (static_cast<uint32_t>(p[5]) << 16);
+          v[j].w = static_cast<uint32_t>(p[6]) | (static_cast<uint32_t>(p[7]) << 16);
         }
       }
     }
+    uint32_t top[4] = {};                  // largest magnitudes of features (2i, 2i + 1)
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      lo = __vmaxu2(lo, v[j].x & 0x7fff7fffu);
-      hi = __vmaxu2(hi, v[j].y & 0x7fff7fffu);
+    for (int j = 0; j < 16; ++j) {
+      top[0] = __vmaxu2(top[0], v[j].x & 0x7fff7fffu);
+      top[1] = __vmaxu2(top[1], v[j].y & 0x7fff7fffu);
+      top[2] = __vmaxu2(top[2], v[j].z & 0x7fff7fffu);
+      top[3] = __vmaxu2(top[3], v[j].w & 0x7fff7fffu);
     }
-    // the codes' magnitudes are integer bits: bf16 exponent field = E (0 for
-    // subnormals, whose block scale is 2^-127 like the least normal's)
-    const uint32_t top[4] = {lo & 0xffffu, lo >> 16, hi & 0xffffu, hi >> 16};
-    uint32_t e[4];
-    uint64_t up[4], up2[4];                // 2^(133 - E) twice, as two factors (one would overflow for E < 6)
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      e[f] = top[f] >> 7;
-      const int s = 133 - static_cast<int>(e[f]);       // -122 .. 133
-      const int s1 = s > 127 ? 127 : s;
-      const float u1 = e[f] >= 255u ? 0.0f : __uint_as_float(static_cast<uint32_t>(s1 + 127) << 23);
-      const float u2 = __uint_as_float(static_cast<uint32_t>(s - s1 + 127) << 23);
-      up[f] = pack_f2(u1, u1);
-      up2[f] = pack_f2(u2, u2);
-    }
+    for (int i = 0; i < 4; ++i) top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], 16));
+    if (!in) continue;
     const uint64_t magic = pack_f2(12582912.0f, 12582912.0f);
-    *reinterpret_cast<uint32_t*>(scales + blk * K + k) = e[0] | (e[1] << 8) | (e[2] << 16) | (e[3] << 24);
+    uint32_t bytes[2] = {};                // the scales
+    uint4* dst = reinterpret_cast<uint4*>(codes + ((blk * 2 + h) * K + k) * 16);
+    uint32_t even[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4* dst = reinterpret_cast<uint4*>(codes + ((blk * 2 + h) * K + k) * 16);
+    for (int f = 0; f < 8; ++f) {
+      // the codes' magnitudes are integer bits: bf16 exponent field = E (0 for
+      // subnormals, whose block scale is 2^-127 like the least normal's)
+      const uint32_t e = ((f & 1) ? top[f >> 1] >> 16 : top[f >> 1] & 0xffffu) >> 7;
+      bytes[f >> 2] |= e << (8 * (f & 3));
+      // 2^(133 - E) as two factors (one would overflow for E < 6)
+      const int s = 133 - static_cast<int>(e);            // -122 .. 133
+      const int s1 = s > 127 ? 127 : s;
+      const float u1 = e >= 255u ? 0.0f : __uint_as_float(static_cast<uint32_t>(s1 + 127) << 23);
+      const float u2 = __uint_as_float(static_cast<uint32_t>(s - s1 + 127) << 23);
+      const uint64_t up = pack_f2(u1, u1), up2 = pack_f2(u2, u2);
+      uint32_t w[4];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        uint32_t w[4];
+      for (int g = 0; g < 4; ++g) {
+        uint32_t c[2];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t c[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {    // tokens 2u, 2u + 1 of the four
-            const uint2 v0 = v[16 * h + 4 * g + 2 * u], v1 = v[16 * h + 4 * g + 2 * u + 1];
-            const uint32_t b0 = f < 2 ? v0.x : v0.y, b1 = f < 2 ? v1.x : v1.y;
-            const uint64_t x2 = (f & 1) ? pack_f2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))
-                                        : pack_f2(__uint_as_float(b0 << 16), __uint_as_float(b1 << 16));
-            // the scaling is exact; adding 1.5 * 2^23 leaves rint(y), -128 .. 128, in the low 16 bits
-            const uint64_t t = add_f2(mul_f2(mul_f2(x2, up[f]), up2[f]), magic);
-            const uint32_t r = __byte_perm(static_cast<uint32_t>(t), static_cast<uint32_t>(t >> 32), 0x5410);
-            c[u] = __vmaxs2(__vmins2(r, 0x007f007fu), 0xff81ff81u);
-          }
-          w[g] = e[f] >= 255u ? 0u : __byte_perm(c[0], c[1], 0x6420);
+        for (int u = 0; u < 2; ++u) {      // tokens 2u, 2u + 1 of the four
+          const uint4 v0 = v[4 * g + 2 * u], v1 = v[4 * g + 2 * u + 1];
+          const uint32_t b0 = f < 2 ? v0.x : f < 4 ? v0.y : f < 6 ? v0.z : v0.w;
+          const uint32_t b1 = f < 2 ? v1.x : f < 4 ? v1.y : f < 6 ? v1.z : v1.w;
+          const uint64_t x2 = (f & 1) ? pack_f2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))
+                                      : pack_f2(__uint_as_float(b0 << 16), __uint_as_float(b1 << 16));
+          // the scaling is exact; adding 1.5 * 2^23 leaves rint(y), -128 .. 128, in the low 16 bits
+          const uint64_t t = add_f2(mul_f2(mul_f2(x2, up), up2), magic);
+          const uint32_t r = __byte_perm(static_cast<uint32_t>(t), static_cast<uint32_t>(t >> 32), 0x5410);
+          c[u] = __vmaxs2(__vmins2(r, 0x007f007fu), 0xff81ff81u);
         }
-        dst[f] = make_uint4(w[0], w[1], w[2], w[3]);
+        w[g] = e >= 255u ? 0u : __byte_perm(c[0], c[1], 0x6420);
+      }
+      if (f & 1) {
+        if (WIDE) {
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + f - 1), "r"(even[0]),
+                       "r"(even[1]), "r"(even[2]), "r"(even[3]), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        } else {
+          dst[f - 1] = make_uint4(even[0], even[1], even[2], even[3]);
+          dst[f] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) even[g] = w[g];
       }
     }
+    if (h == 0) *reinterpret_cast<uint2*>(scales + blk * K + k) = make_uint2(bytes[0], bytes[1]);
   }
 }
 
@@ -216,11 +236,13 @@ dq_status dq_act8_pack(const void* x_bf16, int64_t M, int64_t K, int64_t ldx, in
   if (st != DQ_OK) return st;
   if (M == 0) return DQ_OK;
   const int64_t blks = (M + 31) / 32;
-  const dim3 grid(static_cast<unsigned>((K / 4 + ACT8_THREADS - 1) / ACT8_THREADS), static_cast<unsigned>(blks < 65535 ? blks : 65535));
-  const bool vec = aligned(x_bf16, 8) && ldx % 4 == 0;
-  return launch(vec ? act8_pack_kernel<true> : act8_pack_kernel<false>, grid, ACT8_THREADS,
-                reinterpret_cast<cudaStream_t>(stream), static_cast<const uint16_t*>(x_bf16), M, static_cast<int>(K),
-                ldx, reinterpret_cast<uint8_t*>(codes), scales);
+  const dim3 grid(static_cast<unsigned>((K + 127) / 128), static_cast<unsigned>(blks < 65535 ? blks : 65535));
+  auto k = aligned(x_bf16, 16) && ldx % 8 == 0 ? (aligned(codes, 32) ? act8_pack_kernel<16, true> : act8_pack_kernel<16, false>)
+           : aligned(x_bf16, 8) && ldx % 4 == 0 ? act8_pack_kernel<8, false>
+                                                : act8_pack_kernel<2, false>;
+  return launch(k, grid, ACT8_THREADS, reinterpret_cast<cudaStream_t>(stream),
+                static_cast<const uint16_t*>(x_bf16), M, static_cast<int>(K), ldx, reinterpret_cast<uint8_t*>(codes),
+                scales);
 }
 
 dq_status dq_act8_unpack(const int8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* out_bf16,

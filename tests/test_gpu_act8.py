@@ -54,6 +54,18 @@ def test_pack_and_unpack_bit_exact(M, K, kind):
     assert (np.abs(v - x.double().numpy()) <= step / 2).all()
 
 
+@pytest.mark.parametrize("M,K", [(75, 272), (3, 16)])
+def test_pack_into_codes_aligned_to_16_bytes_only(M, K):
+    g = 2 * -(-M // 32)
+    x = _x(M, K, 6)
+    buf = torch.full((g * K * 16 + 48,), 77, dtype=torch.int8, device="cuda")
+    codes = buf[16:16 + g * K * 16].view(g, K, 16)
+    assert codes.data_ptr() % 32 == 16
+    _, scales = dq.dq_act8_pack(x.cuda(), codes=codes)
+    _check(x, codes, scales)
+    assert bool((buf[:16] == 77).all()) and bool((buf[16 + g * K * 16:] == 77).all())
+
+
 @pytest.mark.parametrize("offset,pad", [(0, 8), (0, 1), (1, 0), (2, 2), (4, 4)])
 def test_pack_strides_and_offsets(offset, pad):
     M, K = 75, 272
