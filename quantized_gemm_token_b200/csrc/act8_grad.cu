@@ -41,7 +41,7 @@
 // workspace, no atomics), in a second launch where whole waves come first.
 // Measured (bound: the MMAs' 512 cycles per step, about 590 reached): 8192 x
 // 4096 x 4096 197 us, 1393 TFLOP/s (0.82 of the measured bf16 burst, 0.97 of
-// the sustained rate); 65792 tokens, 1280 -> 5120, fp32: 619 us, 696 us with db
+// the sustained rate); 65792 tokens, 1280 -> 5120, fp32: 611 us, 641 us with db
 // (dY read again by a kernel of its own: 790 - 870 us); 2048 x 4096 x 4096 53.5 us
 // (256 tiles on 74 pairs; 5 us of it are launch, prologue and ends).
 #include <cuda_bf16.h>
@@ -197,6 +197,15 @@ __device__ __forceinline__ void codes4_top(uint32_t w, uint32_t e, uint32_t& r0,
   const uint32_t two = e == 255u ? 0x7fc07fc0u : 0x40004000u;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r0) : "r"(a), "r"(two));
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r1) : "r"(b), "r"(two));
+}
+
+// Two fp32 sums take a pair of bf16 values (each addition rounds in fp32; the
+// mixed addition saves the conversion: db above 664 us, 679 with shifts and
+// masks; four tokens to one address the rest).
+__device__ __forceinline__ void add_bf16x2(float& lo, float& hi, uint32_t v) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(lo), "+f"(hi)
+      : "r"(v));
 }
 
 struct GradUnit {
@@ -491,23 +500,26 @@ __global__ void __launch_bounds__(WG_THREADS, 1)
       // Column sums: warps w and w + 4 take the steps of ring stages w and w + 4,
       // half of a step's tokens each (so four steps are summed at a time), a
       // lane the 8 channels of 16-byte unit lane % (units per row) of every
-      // second (or fourth) token.
+      // second (or fourth) token of eight.
       const int unit = lane & (half_n / 8 - 1);
       const int tstep = 256 / half_n;
-      const int tok0 = lane / (half_n / 8) + (ew >> 2) * (WG_STEP / 2);
+      const int tok0 = lane / (half_n / 8);
       float col[8] = {};
       auto sum_stage = [&](int st) {             // false: the wait failed
         if (!mbar_wait_warp(smem_u32(ydone + st), (dphase >> st) & 1u, g.wait, abort_flag)) return false;
         dphase ^= 1u << st;
-        const uint32_t sy = base + static_cast<uint32_t>(st) * y_bytes + static_cast<uint32_t>(unit >> 3) * 8192u;
-#pragma unroll 4
-        for (int m = 0; m < WG_STEP / 2; m += tstep) {
-          const uint4 v = pipe::lds128(sy + pipe::sw128_off(tok0 + m, unit & 7));
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t sy = base + static_cast<uint32_t>(st) * y_bytes + static_cast<uint32_t>(unit >> 3) * 8192u +
+                            static_cast<uint32_t>(ew >> 2) * (WG_STEP / 2 * 128);
+        for (int tok = tok0; tok < 8; tok += tstep) {
+          // (rows eight apart share their swizzle)
+          const uint32_t row = sy + pipe::sw128_off(tok, unit & 7);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            col[2 * i] += __uint_as_float(x[i] << 16);
-            col[2 * i + 1] += __uint_as_float(x[i] & 0xffff0000u);
+          for (int i = 0; i < WG_STEP / 16; ++i) {
+            const uint4 v = pipe::lds128(row + 1024u * i);
+            add_bf16x2(col[0], col[1], v.x);
+            add_bf16x2(col[2], col[3], v.y);
+            add_bf16x2(col[4], col[5], v.z);
+            add_bf16x2(col[6], col[7], v.w);
           }
         }
         __syncwarp();
