@@ -435,7 +435,8 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
  *   stride ldq bytes), sf, s_row fp32 [M] (NV; ignored for MX, may be NULL).
  *   Rows with ldx % 8 == 0, a 16-byte aligned x, 8-byte aligned q and ldq and
  *   K <= 32768 take the single-pass kernel, others a slower one.
- * dq_quantize_weight_fp4: the same for fp32 rows (output channels).
+ * dq_quantize_weight_fp4: the same for fp32 rows (output channels); the
+ *   single-pass kernel takes ldw % 4 == 0 and K <= 16384.
  * dq_fp4_dequantize: out bf16 [M, K] = bf16(fp32(e2m1 * d) * s); s may be
  *   NULL (1).  Exact for what the quantizers write (an NV value above bf16's
  *   largest, from a row that reaches it, becomes an infinity).

@@ -19,7 +19,8 @@
 // Both are bound by HBM: one pass over x, 0.53 or 0.56 bytes written for 2
 // read.  A row stays in registers between the row maximum and the codes.
 // Measured, 16384 x 8192: nv 53.3 us (6.45 TB/s, 1.00 of the measured copy
-// rate), mx 49.0 us (6.94 TB/s; the mix reads more than it writes).
+// rate), mx 49.0 us (6.94 TB/s; the mix reads more than it writes); fp32
+// weights, 28672 x 8192: 151 us (7.1 TB/s), nv and mx.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -99,25 +100,31 @@ __device__ __forceinline__ uint32_t e2m1_by_borders(float ax, float d, bool neg)
   return c | (neg ? 8u : 0u);
 }
 
-// ---------------------------------------------------------------- bf16 rows
-__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, bool wide) {
-  if (wide) {
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
-  } else {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p)), b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-    w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+// ---------------------------------------------------------------- rows
+// A run of 16 features: 32 bytes of bf16, 64 of fp32, as 32-bit words.
+template <bool WIDE, int W>
+__device__ __forceinline__ void load_run(uint32_t (&w)[W], const void* p) {
+#pragma unroll
+  for (int i = 0; i < W; i += 8) {
+    const char* a = static_cast<const char*>(p) + 4 * i;
+    if (WIDE) {
+      asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                     "=r"(w[i + 6]), "=r"(w[i + 7])
+                   : "l"(a));
+    } else {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(a)), v = __ldcs(reinterpret_cast<const uint4*>(a) + 1);
+      w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+      w[i + 4] = v.x, w[i + 5] = v.y, w[i + 6] = v.z, w[i + 7] = v.w;
+    }
   }
 }
 
-// Register-resident: 2^tpr_log2 (32..256) threads own a row, up to VPT runs of
-// 16 features (32 bytes, one load) each: an NV block is one run, an MX block
-// two neighbouring lanes'.
+// Register-resident: 2^tpr_log2 (8..256) threads own a row, up to VPT runs of
+// 16 features each: an NV block is one run, an MX block two neighbouring lanes'.
 //
-// For NV, two roundings are decided without a division, both because bf16 has
-// 8 significant bits.  (1) The e4m3 scale of t / 6, t = a / s exact: a rounding
+// For NV and bf16 rows, two roundings are decided without a division, both because
+// bf16 has 8 significant bits.  (1) The e4m3 scale of t / 6, t = a / s exact: a rounding
 // border B of e4m3 has 5 significant bits and 6 B at most 7, so t / 6 is either
 // exactly a border or at least 2^-8 (relative) away from it; t * fp32(1/6) is
 // within 2^-23 of t / 6, so rounding it to 12 significant bits restores the
@@ -127,11 +134,19 @@ __device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, bool
 // X / d is a border or at least 2^-10 away from it (2^-8 relative, the least
 // border being 1/4), and rounding to a multiple of 2^-10 (adding and
 // subtracting 1.5 * 2^13) again restores ties and crosses nothing.
-template <bool NV, int VPT, bool WIDE>
-__global__ void __launch_bounds__(256) fp4_rows_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+//
+// fp32 rows: the block's scale by a division; the code from the fp32 quotient X / d with
+// Markstein's correction (q = X c, c = fp32(1 / d); r = X - q d, exact; q + r c), which is
+// RN(X / d (1 + e)), |e| < 2^-45.  A border B is met only if X / d is B: else
+// X differs from B d (at most 7 significant bits) by at least its own last
+// place, so X / d is 2 / m (m < 1.9 the mantissa of d) half places or more away from B.
+template <typename T, bool NV, int VPT, bool WIDE>
+__global__ void __launch_bounds__(256) fp4_rows_kernel(const T* __restrict__ x, int64_t M, int64_t K,
                                                        int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
                                                        uint8_t* __restrict__ sf, int64_t sf_atoms,
                                                        float* __restrict__ s_row, int tpr_log2) {
+  constexpr bool F32 = sizeof(T) == 4;
+  constexpr int W = F32 ? 16 : 8;
   griddep_launch_dependents();
   griddep_wait();
   const int tpr = 1 << tpr_log2;
@@ -142,32 +157,41 @@ __global__ void __launch_bounds__(256) fp4_rows_kernel(const uint16_t* __restric
   const bool in = row < M;               // rows up to the next multiple of 128 get zero scales
   __shared__ uint32_t warp_max[8];
 
-  uint32_t v[VPT][8];
-  const uint16_t* xr = x + row * ldx;
+  uint32_t v[VPT][W];
+  const T* xr = x + row * ldx;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int u = t + i * tpr;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0u;
-    if (in && u < nu) load16(v[i], xr + u * 16, WIDE);
+    for (int j = 0; j < W; ++j) v[i][j] = 0u;
+    if (in && u < nu) load_run<WIDE>(v[i], xr + u * 16);
   }
   // magnitudes order like their bits, NaN above infinity above the rest
   uint32_t top[VPT];
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    uint32_t m = v[i][0] & 0x7fff7fffu;
+    uint32_t b;
+    if constexpr (F32) {
+      b = v[i][0] & 0x7fffffffu;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) m = __vmaxu2(m, v[i][j] & 0x7fff7fffu);
-    uint32_t b = max(m & 0xffffu, m >> 16);
+      for (int j = 1; j < W; ++j) b = max(b, v[i][j] & 0x7fffffffu);
+    } else {
+      uint32_t m = v[i][0] & 0x7fff7fffu;
+#pragma unroll
+      for (int j = 1; j < W; ++j) m = __vmaxu2(m, v[i][j] & 0x7fff7fffu);
+      b = max(m & 0xffffu, m >> 16) << 16;
+    }
     if (!NV) b = max(b, __shfl_xor_sync(0xffffffffu, b, 1));
-    top[i] = b << 16;                    // fp32 bits
-    amax = max(amax, top[i]);
+    top[i] = b;                          // fp32 bits
+    amax = max(amax, b);
   }
   float inv_s = 1.0f;
   bool bad_row = false;
   if constexpr (NV) {
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    if (tpr >= 32) amax = __reduce_max_sync(0xffffffffu, amax);
+    else
+      for (int o = tpr >> 1; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (tpr > 32) {
       const int warp = threadIdx.x >> 5;
       if ((threadIdx.x & 31) == 0) warp_max[warp] = amax;
@@ -187,29 +211,48 @@ __global__ void __launch_bounds__(256) fp4_rows_kernel(const uint16_t* __restric
   for (int i = 0; i < VPT; ++i) {
     const int u = t + i * tpr;
     uint32_t byte;
-    float c;
+    float c = 0.0f, d = 0.0f;
     bool zero;
     if constexpr (NV) {
-      const uint32_t r = __float_as_uint(__uint_as_float(top[i]) * inv_s * (1.0f / 6.0f));
-      byte = bad_row ? 0u : e4m3_byte(__uint_as_float((r + 0x800u) & 0xfffff000u));
+      const float a = __uint_as_float(top[i]) * inv_s;
+      uint32_t r;
+      if constexpr (F32) r = __float_as_uint(__fdiv_rn(a, 6.0f));
+      else r = (__float_as_uint(a * (1.0f / 6.0f)) + 0x800u) & 0xfffff000u;
+      byte = bad_row ? 0u : e4m3_byte(__uint_as_float(r));
       zero = byte == 0;
-      float rcp;
-      asm("rcp.approx.f32 %0, %1;" : "=f"(rcp) : "f"(e4m3_value(byte)));
-      c = zero ? 0.0f : rcp * inv_s;
+      d = e4m3_value(byte);
+      if constexpr (F32) {
+        c = __frcp_rn(d);
+      } else {
+        float rcp;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(rcp) : "f"(d));
+        c = zero ? 0.0f : rcp * inv_s;
+      }
     } else {
       byte = mx_scale(top[i], c);
       zero = byte == 255u;
     }
-    const uint64_t c2 = pack_f2(c, c), up = pack_f2(12288.0f, 12288.0f), down = pack_f2(-12288.0f, -12288.0f);
     uint32_t codes[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const uint64_t c2 = pack_f2(c, c), up = pack_f2(12288.0f, 12288.0f), down = pack_f2(-12288.0f, -12288.0f);
       float y[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t w = v[i][4 * h + j];
-        uint64_t p = mul_f2(pack_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), c2);
-        if constexpr (NV) p = add_f2(add_f2(p, up), down);
+        uint64_t p;
+        if constexpr (F32) {
+          p = pack_f2(__uint_as_float(v[i][8 * h + 2 * j]), __uint_as_float(v[i][8 * h + 2 * j + 1]));
+          if constexpr (NV) {
+            const uint64_t X = mul_f2(p, pack_f2(inv_s, inv_s)), quot = mul_f2(X, c2);
+            p = fma_f2(fma_f2(quot, pack_f2(-d, -d), X), c2, quot);
+          } else {
+            p = mul_f2(p, c2);
+          }
+        } else {
+          const uint32_t w = v[i][4 * h + j];
+          p = mul_f2(pack_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), c2);
+          if constexpr (NV) p = add_f2(add_f2(p, up), down);
+        }
         unpack_f2(p, y[2 * j], y[2 * j + 1]);
       }
       codes[h] = zero ? 0u : e2m1x8(y);
@@ -237,7 +280,7 @@ __device__ __forceinline__ float elem_f32<float>(const float* p) {
   return *p;
 }
 
-// Any stride, alignment or row length, and fp32 weights: one CTA per row, two
+// Any stride, alignment or row length: one CTA per row, two
 // passes over the row (the second from L2).  A thread takes one group of four
 // blocks at a time, so a scale word has one writer.
 template <typename T, bool NV>
@@ -411,24 +454,27 @@ dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, in
                    cudaStream_t stream) {
   const int64_t rows = (M + 127) / 128 * 128;
   const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
-  if constexpr (sizeof(T) == 2) {
-    if (K <= 32768 && ldx % 8 == 0 && aligned(x, 16) && ldq % 8 == 0 && aligned(q, 8)) {
-      // Runs per thread: four for NV (fewer threads share the row maximum: 16384 x 8192 53.4 us against 57.5 with
-      // two, 65792 x 1280 43.3 against 51.3), two for MX (49.1 against 53.9, 37.7 against 43.1), more where 256
-      // threads would not hold the row
-      const int64_t nu = K / 16;
-      int vpt = nu <= 32 ? 1 : !NV || nu <= 64 ? 2 : 4;
-      int lg = 5;
-      while (lg < 8 && (static_cast<int64_t>(vpt) << lg) < nu) ++lg;
-      while ((static_cast<int64_t>(vpt) << lg) < nu) vpt *= 2;
-      const int64_t blocks = (rows + (256 >> lg) - 1) / (256 >> lg);
-      const bool wide = aligned(x, 32) && ldx % 16 == 0;
-      auto k = vpt == 1   ? (wide ? fp4_rows_kernel<NV, 1, true> : fp4_rows_kernel<NV, 1, false>)
-               : vpt == 2 ? (wide ? fp4_rows_kernel<NV, 2, true> : fp4_rows_kernel<NV, 2, false>)
-               : vpt == 4 ? (wide ? fp4_rows_kernel<NV, 4, true> : fp4_rows_kernel<NV, 4, false>)
-                          : (wide ? fp4_rows_kernel<NV, 8, true> : fp4_rows_kernel<NV, 8, false>);
-      return launch(k, blocks, stream, x, M, K, ldx, q, ldq, sf, atoms, s_row, lg);
+  constexpr int V = 16 / sizeof(T);                      // elements per 16 bytes
+  if (K <= 4096 * V && ldx % V == 0 && aligned(x, 16) && ldq % 8 == 0 && aligned(q, 8)) {
+    // Runs per thread: four for NV and bf16 (fewer threads share the row maximum: 16384 x 8192 53.4 us against 57.5
+    // with two, 65792 x 1280 43.3 against 51.3), two for MX (49.1 against 53.9, 37.7 against 43.1) and for fp32 (28672
+    // x 8192 nv 151 against 179 with four), more where 256 threads would not hold the row.  Short rows share a warp
+    // (65792 x 64: 5.0 us, 14.8 with a warp per row).
+    const int64_t nu = K / 16;
+    int vpt = nu <= 32 ? 1 : !NV || sizeof(T) == 4 || nu <= 64 ? 2 : 4;
+    int lg = 3;
+    while (lg < 8 && (static_cast<int64_t>(vpt) << lg) < nu) ++lg;
+    if (vpt > 1 && lg < 5) lg = 5;
+    while ((static_cast<int64_t>(vpt) << lg) < nu) vpt *= 2;
+    const int64_t blocks = (rows + (256 >> lg) - 1) / (256 >> lg);
+    const bool wide = aligned(x, 32) && ldx % (2 * V) == 0;
+    auto k = vpt == 1   ? (wide ? fp4_rows_kernel<T, NV, 1, true> : fp4_rows_kernel<T, NV, 1, false>)
+             : vpt == 2 ? (wide ? fp4_rows_kernel<T, NV, 2, true> : fp4_rows_kernel<T, NV, 2, false>)
+                        : (wide ? fp4_rows_kernel<T, NV, 4, true> : fp4_rows_kernel<T, NV, 4, false>);
+    if constexpr (sizeof(T) == 2) {                      // (fp32 rows end at four)
+      if (vpt == 8) k = wide ? fp4_rows_kernel<T, NV, 8, true> : fp4_rows_kernel<T, NV, 8, false>;
     }
+    return launch(k, blocks, stream, x, M, K, ldx, q, ldq, sf, atoms, s_row, lg);
   }
   return launch(fp4_generic_kernel<T, NV>, rows < kMaxGrid ? rows : kMaxGrid, stream, x, M, rows, K, ldx, q, ldq, sf,
                 atoms, s_row);

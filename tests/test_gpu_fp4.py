@@ -110,6 +110,50 @@ def test_quantize_weight_bit_exact(N, K, kind, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("kind", ["normal", "wide", "ties", "edges"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R,K", [(300, 64), (257, 128), (200, 192), (131, 256), (70, 544)])
+def test_quantize_short_rows(R, K, dtype, kind, fmt):
+    """Rows that share a warp: 8, 16 or 32 threads each."""
+    x = _x(R, K, R + K, kind, dtype)
+    f = dq.dq_quantize_rows_fp4 if dtype == torch.bfloat16 else dq.dq_quantize_weight_fp4
+    _check_quantized(x, fmt, *f(x.cuda(), fmt))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("kind", ["normal", "outliers", "wide", "edges"])
+@pytest.mark.parametrize("N,K", [(130, 1280), (9, 8192), (3, 16384), (2, 16416)])
+def test_quantize_long_weight_rows(N, K, kind, fmt):
+    w = _x(N, K, N + K, kind, torch.float32)
+    _check_quantized(w, fmt, *dq.dq_quantize_weight_fp4(w.cuda(), fmt))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("offset,pad", [(0, 8), (0, 4), (0, 3), (1, 0), (4, 4)])
+def test_quantize_weight_strides_and_offsets(offset, pad, fmt):
+    N, K = 37, 416
+    w = _x(N, K + pad + offset, 5, "wide", torch.float32).cuda()[:, offset:offset + K]
+    _check_quantized(w.cpu(), fmt, *dq.dq_quantize_weight_fp4(w, fmt))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_fp32_values_beside_a_border(fmt):
+    """Every rounding border of a code times every mantissa step of the block
+    scale, the fp32 values next to it on either side, and their negatives."""
+    rows = []
+    borders = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    for d in (8, 9, 10, 11, 12, 13, 14, 15):
+        b = borders * (d * 2.0 ** -4)
+        near = torch.stack([torch.nextafter(b, torch.zeros(7)), b, torch.nextafter(b, torch.full((7,), 9.0))]).flatten()
+        near = torch.cat([near, -near, torch.zeros(3)])
+        for part in near.split(15):
+            rows.append(torch.cat([torch.tensor([6.0 * d * 2.0 ** -4]), part]))
+    w = torch.stack(rows)
+    w = torch.cat([w, torch.zeros((-w.shape[0] % 4, 16))]).view(-1, 64)
+    _check_quantized(w, fmt, *dq.dq_quantize_weight_fp4(w.cuda(), fmt))
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("offset,pad", [(0, 8), (0, 3), (1, 0), (4, 12)])
 def test_quantize_strides_and_offsets(offset, pad, fmt):
     """Column slices of a wider matrix, aligned or not, and a strided q."""
