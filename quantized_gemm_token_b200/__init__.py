@@ -132,8 +132,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-# The current stream's handle without building a torch.cuda.Stream (10 us a call).
+# The current stream's handle without building a torch.cuda.Stream (10 us a call),
+# and the current device of an initialised process.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
@@ -700,9 +702,14 @@ def _here(t: torch.Tensor, name: str) -> int:
     dev = t.get_device() if isinstance(t, torch.Tensor) else -1
     if dev < 0:
         raise TypeError(f"{name}: expected a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if dev != _device():
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{_device()}")
     return dev
+
+
+def _on(stream, dev: int):
+    """The handle of `stream`, or of the current stream of the current device `dev`."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _arg(t, dtype, shape, dev: int, name: str):
@@ -726,9 +733,10 @@ def _rows(x: torch.Tensor, dtype, name: str):
     not overlap."""
     if x.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
-    if x.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dims, got {x.dim()}")
-    R, C = x.shape
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected 2 dims, got {len(shape)}")
+    R, C = shape
     ld, step = x.stride()
     if step != 1 and C != 1:
         raise ValueError(f"{name}: rows must be contiguous")
@@ -769,7 +777,7 @@ def _quantize_fp4(fn, name, x, dtype, fmt, q, sf, s, stream):
             _arg(s, torch.float32, (M,), dev, "row scales")
     elif s is not None:
         raise ValueError("the mx format has no row scales")
-    _check(fn(x.data_ptr(), M, K, ld, code, q.data_ptr(), ldq, sf.data_ptr(), _ptr(s), _stream(stream)), name)
+    _check(fn(x.data_ptr(), M, K, ld, code, q.data_ptr(), ldq, sf.data_ptr(), _ptr(s), _on(stream, dev)), name)
     return q, sf, s
 
 
@@ -804,7 +812,7 @@ def dq_fp4_tile_scales(scales: torch.Tensor, fmt="nv", sf: torch.Tensor = None, 
     if sf is None:
         sf = _new(shape, torch.uint8, scales, stream)
     _arg(sf, torch.uint8, shape, dev, "sf")
-    _check(lib.dq_fp4_tile_scales(_ptr(scales), R, K, code, _ptr(sf), _stream(stream)), "dq_fp4_tile_scales")
+    _check(lib.dq_fp4_tile_scales(_ptr(scales), R, K, code, _ptr(sf), _on(stream, dev)), "dq_fp4_tile_scales")
     return sf
 
 
@@ -831,7 +839,7 @@ def dq_fp4_dequantize(q, sf, s=None, fmt="nv", out=None, stream=None) -> torch.T
         out = _new((M, K), torch.bfloat16, q, stream)
     else:
         _arg(out, torch.bfloat16, (M, K), dev, "out")
-    _check(lib.dq_fp4_dequantize(q.data_ptr(), sf.data_ptr(), _ptr(s), M, K, code, out.data_ptr(), _stream(stream)),
+    _check(lib.dq_fp4_dequantize(q.data_ptr(), sf.data_ptr(), _ptr(s), M, K, code, out.data_ptr(), _on(stream, dev)),
            "dq_fp4_dequantize")
     return out
 
@@ -863,7 +871,7 @@ def dq_fp4_linear(A, sfa, s_row, W, sfw, s_col, bias=None, fmt="nv", out=None, o
     else:
         _arg(out, odt, (M, N), dev, "out")
     _check(lib.dq_fp4_linear(A.data_ptr(), sfa.data_ptr(), _ptr(s_row), M, K, W.data_ptr(), sfw.data_ptr(),
-                             _ptr(s_col), N, code, _ptr(bias), out.data_ptr(), oc, _stream(stream)),
+                             _ptr(s_col), N, code, _ptr(bias), out.data_ptr(), oc, _on(stream, dev)),
            "dq_fp4_linear")
     return out
 
@@ -898,7 +906,7 @@ def dq_act8_pack(x: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tens
         scales = _new((g, K), torch.uint8, x, stream)
     else:
         _arg(scales, torch.uint8, (g, K), dev, "scales")
-    _check(lib.dq_act8_pack(x.data_ptr(), M, K, ld, codes.data_ptr(), scales.data_ptr(), _stream(stream)),
+    _check(lib.dq_act8_pack(x.data_ptr(), M, K, ld, codes.data_ptr(), scales.data_ptr(), _on(stream, dev)),
            "dq_act8_pack")
     return codes, scales
 
@@ -911,7 +919,7 @@ def dq_act8_unpack(codes, scales, M: int, out=None, stream=None) -> torch.Tensor
         out = _new((M, K), torch.bfloat16, codes, stream)
     else:
         _arg(out, torch.bfloat16, (M, K), dev, "out")
-    _check(lib.dq_act8_unpack(codes.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(), _stream(stream)),
+    _check(lib.dq_act8_unpack(codes.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(), _on(stream, dev)),
            "dq_act8_unpack")
     return out
 
@@ -943,7 +951,7 @@ def dq_act8_weight_grad(dy, codes, scales, out=None, out_dtype="bf16", accumulat
     if M <= 1:                        # a single row has no stride to speak of
         ld = (ld + 7) // 8 * 8
     _check(lib.dq_act8_weight_grad(dy.data_ptr(), M, N, ld, codes.data_ptr(), scales.data_ptr(), K, out.data_ptr(),
-                                   oc, int(accumulate), _ptr(db), _stream(stream)), "dq_act8_weight_grad")
+                                   oc, int(accumulate), _ptr(db), _on(stream, dev)), "dq_act8_weight_grad")
     return out, db
 
 
