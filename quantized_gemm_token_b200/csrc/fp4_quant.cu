@@ -250,8 +250,8 @@ __global__ void __launch_bounds__(256) fp4_rows_kernel(const T* __restrict__ x, 
           }
         } else {
           const uint32_t w = v[i][4 * h + j];
-          p = mul_f2(pack_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), c2);
-          if constexpr (NV) p = add_f2(add_f2(p, up), down);
+          p = pack_f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+          p = NV ? add_f2(fma_f2(p, c2, up), down) : mul_f2(p, c2);
         }
         unpack_f2(p, y[2 * j], y[2 * j + 1]);
       }
@@ -351,59 +351,62 @@ __global__ void __launch_bounds__(256) fp4_generic_kernel(const T* __restrict__ 
 
 // ---------------------------------------------------------------- dequantize
 // A block takes 512 runs of 16 codes, a thread two of them with all their
-// loads in flight: w = bf16((e2m1 * d) * s), the block product exact.  HBM
+// loads in flight: w = bf16((e2m1 * d) * s).  The block product is exact: for
+// NV in fp16 (six significant bits, 2^-10 .. 2688), two at a time.  HBM
 // bound (16384 x 8192, nv: 52.5 us, 1.02 of the copy rate; 61.9 with one run
 // per thread).  WIDE: a 32-byte aligned output, one store per run.
+// A run's row: rows have per_row runs; inv = floor(2^64 / per_row) + 1, so
+// the high half of i * inv is i / per_row for i * per_row < 2^64 (any matrix that
+// fits the memory).
 constexpr int DEQ_RUNS = 2;
 template <bool NV, bool WIDE>
 __global__ void __launch_bounds__(256) fp4_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
-                                                          const float* __restrict__ s_row, int64_t M, int64_t K,
-                                                          int64_t sf_atoms, uint16_t* __restrict__ out) {
+                                                          const float* __restrict__ s_row, int64_t n, uint32_t per_row,
+                                                          uint64_t inv, int64_t sf_atoms, uint16_t* __restrict__ out) {
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t per_row = static_cast<uint32_t>(K / 16);
-  const int64_t n = M * per_row;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * DEQ_RUNS); i0 < n;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * DEQ_RUNS) + threadIdx.x; i0 < n;
        i0 += static_cast<int64_t>(gridDim.x) * (256 * DEQ_RUNS)) {
-    const int64_t row0 = i0 / per_row;
-    const uint32_t u0 = static_cast<uint32_t>(i0 - row0 * per_row);
     uint2 c[DEQ_RUNS];
     uint32_t byte[DEQ_RUNS];
     float s[DEQ_RUNS];
 #pragma unroll
     for (int j = 0; j < DEQ_RUNS; ++j) {
-      const uint32_t x = threadIdx.x + 256u * j;
-      if (i0 + x >= n) continue;
-      const uint32_t dr = (u0 + x) / per_row;
-      const uint32_t u = u0 + x - dr * per_row;
-      const int64_t row = row0 + dr;
-      c[j] = __ldcs(reinterpret_cast<const uint2*>(q + (i0 + x) * 8));
+      const int64_t i = i0 + 256 * j;
+      if (i >= n) continue;
+      const int64_t row = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(i), inv));
+      const uint32_t u = static_cast<uint32_t>(i) - static_cast<uint32_t>(row) * per_row;
+      c[j] = __ldcs(reinterpret_cast<const uint2*>(q + i * 8));
       const uint32_t blk = NV ? u : u >> 1;
       byte[j] = __ldg(sf + ((row >> 7) * sf_atoms + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3));
       s[j] = s_row != nullptr ? __ldg(s_row + row) : 1.0f;
     }
 #pragma unroll
     for (int j = 0; j < DEQ_RUNS; ++j) {
-      const uint32_t x = threadIdx.x + 256u * j;
-      if (i0 + x >= n) continue;
-      float d;
-      if (NV) d = e4m3_value(byte[j]);
+      const int64_t i = i0 + 256 * j;
+      if (i >= n) continue;
+      uint32_t d2 = 0;                     // NV: d twice, fp16
+      float d = 0.0f;
+      if (NV) asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.f16x2.e4m3x2 %0, %1;\n\tmov.b32 {l, h}, %0;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(d2) : "h"(static_cast<uint16_t>(byte[j])));
       else d = byte[j] == 255u ? __uint_as_float(0x7fc00000u) : pow2i(static_cast<int>(byte[j]) - 127);
+      const uint64_t s2 = pack_f2(s[j], s[j]), df2 = pack_f2(d, d);
       uint32_t o[8];
 #pragma unroll
       for (int h = 0; h < 8; ++h) {
         const uint32_t b = ((h < 4 ? c[j].x : c[j].y) >> (8 * (h & 3))) & 0xffu;
         uint32_t h2;
         asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(h2) : "r"(b));
+        if (NV) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h2) : "r"(d2));
         float lo, hi;
         asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
             : "=f"(lo), "=f"(hi)
             : "r"(h2));
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-            : "=r"(o[h])
-            : "f"(__fmul_rn(__fmul_rn(hi, d), s[j])), "f"(__fmul_rn(__fmul_rn(lo, d), s[j])));
+        uint64_t p = pack_f2(lo, hi);
+        if (!NV) p = mul_f2(p, df2);
+        unpack_f2(mul_f2(p, s2), lo, hi);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[h]) : "f"(hi), "f"(lo));
       }
-      uint16_t* dst = out + (i0 + x) * 16;
+      uint16_t* dst = out + i * 16;
       if (WIDE) {
         asm volatile("st.global.L1::no_allocate.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]),
                      "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
@@ -535,7 +538,9 @@ dq_status dq_fp4_dequantize(const uint8_t* q, const uint8_t* sf, const float* s,
   const bool wide = aligned(out_bf16, 32);
   auto k = fmt == DQ_FP4_NV ? (wide ? fp4_dequant_kernel<true, true> : fp4_dequant_kernel<true, false>)
                             : (wide ? fp4_dequant_kernel<false, true> : fp4_dequant_kernel<false, false>);
-  return launch(k, blocks, cs, q, sf, s, M, K, fp4_atoms(K, fmt), static_cast<uint16_t*>(out_bf16));
+  const uint64_t per_row = static_cast<uint64_t>(K / 16);   // (2 at least: K % 32 == 0)
+  return launch(k, blocks, cs, q, sf, s, M * (K / 16), per_row, ~uint64_t(0) / per_row + 1, fp4_atoms(K, fmt),
+                static_cast<uint16_t*>(out_bf16));
 }
 
 dq_status dq_fp4_tile_scales(const uint8_t* scales, int64_t rows, int64_t K, int fmt, uint8_t* sf, dq_stream_t stream) {
