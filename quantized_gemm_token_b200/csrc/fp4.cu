@@ -624,7 +624,8 @@ __global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < C::CHUNKS; ++i) {
         const int c = grp + i * GROUPS;
-        if (c < nch)
+        // a block wholly past the matrix is not stored and takes no buffer: the wait for a buffer counts stores
+        if (c < nch && n0 + c * 32 < g.N && m_slab < g.M)
           store_row_chunk_staged<true>(g, &tm_c, next_buf(), lane, m_slab, n0 + c * 32, r[i], srow, sc_slot, c * 32);
       }
       __syncwarp();

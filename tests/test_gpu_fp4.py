@@ -112,9 +112,11 @@ def test_quantize_weight_bit_exact(N, K, kind, fmt):
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("kind", ["normal", "wide", "ties", "edges"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("R,K", [(300, 64), (257, 128), (200, 192), (131, 256), (70, 544)])
-def test_quantize_short_rows(R, K, dtype, kind, fmt):
-    """Rows that share a warp: 8, 16 or 32 threads each."""
+@pytest.mark.parametrize("R,K", [(300, 64), (257, 128), (200, 192), (131, 256), (70, 544), (33, 640), (40, 768),
+                                 (19, 2560), (20, 3584), (9, 5120), (7, 6112), (3, 12288), (2, 20480)])
+def test_quantize_rows_of_every_split(R, K, dtype, kind, fmt):
+    """Rows that share a warp (8 or 16 threads each), and one to eight runs of 16
+    features per thread, filled or with idle places."""
     x = _x(R, K, R + K, kind, dtype)
     f = dq.dq_quantize_rows_fp4 if dtype == torch.bfloat16 else dq.dq_quantize_weight_fp4
     _check_quantized(x, fmt, *f(x.cuda(), fmt))
@@ -245,6 +247,22 @@ def test_few_tokens(M, N, K, fmt):
                                    (1024, 2048, 736), (1799, 1280, 1280), (2300, 4104, 288), (2048, 4096, 4096)])
 def test_many_tokens(M, N, K, fmt):
     _check_product(M, N, K, fmt, bias=M % 2 == 1, seed=M)
+
+
+@pytest.mark.parametrize("N", [4104, 4136, 4168, 4200, 8])
+@pytest.mark.parametrize("K", [32, 288])
+def test_ragged_last_tiles_in_quick_succession(N, K):
+    """Blocks of the output past the last column are not stored and must not
+    disturb the ones still being stored: with few features the tiles follow one
+    another at once, and the first calls run cold."""
+    M = 5000
+    x, w = _x(M, K, N).cuda(), _x(N, K, N + 1, dtype=torch.float32).cuda()
+    A, W = dq.dq_quantize_rows_fp4(x, "mx"), dq.dq_quantize_weight_fp4(w, "mx")
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    want = dq.dq_fp4_linear(*A, *W, fmt="mx", out_dtype="f32").bfloat16()
+    for _ in range(5):
+        flush.fill_(1)
+        assert torch.equal(dq.dq_fp4_linear(*A, *W, fmt="mx"), want)
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
