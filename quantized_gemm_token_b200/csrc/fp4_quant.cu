@@ -452,6 +452,11 @@ dq_status launch(void (*kernel)(P...), int64_t blocks, cudaStream_t stream, A...
 
 constexpr int64_t kMaxGrid = 1 << 20;
 
+template <typename T, bool NV, int VPT>
+auto rows_kernel(bool wide) {
+  return wide ? fp4_rows_kernel<T, NV, VPT, true> : fp4_rows_kernel<T, NV, VPT, false>;
+}
+
 template <typename T, bool NV>
 dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* sf, float* s_row,
                    cudaStream_t stream) {
@@ -460,22 +465,36 @@ dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, in
   constexpr int V = 16 / sizeof(T);                      // elements per 16 bytes
   if (K <= 4096 * V && ldx % V == 0 && aligned(x, 16) && ldq % 8 == 0 && aligned(q, 8)) {
     // Runs per thread: four for NV and bf16 (fewer threads share the row maximum: 16384 x 8192 53.4 us against 57.5
-    // with two, 65792 x 1280 43.3 against 51.3), two for MX (49.1 against 53.9, 37.7 against 43.1) and for fp32 (28672
-    // x 8192 nv 151 against 179 with four), more where 256 threads would not hold the row.  Short rows share a warp
+    // with two), two for MX (49.1 against 53.9 with four) and for fp32 (28672 x 8192 nv 151 against 179 with four), more
+    // where 256 threads would not hold the row; three, or for NV and bf16 five, where that leaves fewer idle places
+    // (65792 x 1280: nv 34.4 us with five, 44.3 with four; mx 33.0 with three, 37.9 with two).  Short rows share a warp
     // (65792 x 64: 5.0 us, 14.8 with a warp per row).
     const int64_t nu = K / 16;
-    int vpt = nu <= 32 ? 1 : !NV || sizeof(T) == 4 || nu <= 64 ? 2 : 4;
-    int lg = 3;
-    while (lg < 8 && (static_cast<int64_t>(vpt) << lg) < nu) ++lg;
-    if (vpt > 1 && lg < 5) lg = 5;
-    while ((static_cast<int64_t>(vpt) << lg) < nu) vpt *= 2;
+    constexpr bool four = NV && sizeof(T) == 2;
+    auto threads_log2 = [nu](int v) {
+      int lg = 3;
+      while (lg < 8 && (static_cast<int64_t>(v) << lg) < nu) ++lg;
+      return lg;
+    };
+    int vpt = nu <= 32 ? 1 : four && nu > 64 ? 4 : 2;
+    while ((static_cast<int64_t>(vpt) << 8) < nu) vpt *= 2;
+    int lg = threads_log2(vpt);
+    for (int v = four ? 5 : 3; v >= 3 && nu > 32; v -= 2) {
+      const int l = threads_log2(v);
+      if ((static_cast<int64_t>(v) << l) >= nu && 10 * (v << l) < 9 * (vpt << lg)) {
+        vpt = v;
+        lg = l;
+      }
+    }
     const int64_t blocks = (rows + (256 >> lg) - 1) / (256 >> lg);
     const bool wide = aligned(x, 32) && ldx % (2 * V) == 0;
-    auto k = vpt == 1   ? (wide ? fp4_rows_kernel<T, NV, 1, true> : fp4_rows_kernel<T, NV, 1, false>)
-             : vpt == 2 ? (wide ? fp4_rows_kernel<T, NV, 2, true> : fp4_rows_kernel<T, NV, 2, false>)
-                        : (wide ? fp4_rows_kernel<T, NV, 4, true> : fp4_rows_kernel<T, NV, 4, false>);
+    auto k = vpt == 1 ? rows_kernel<T, NV, 1>(wide) : vpt == 2 ? rows_kernel<T, NV, 2>(wide)
+             : vpt == 3 ? rows_kernel<T, NV, 3>(wide) : rows_kernel<T, NV, 4>(wide);
+    if constexpr (four) {
+      if (vpt == 5) k = rows_kernel<T, NV, 5>(wide);
+    }
     if constexpr (sizeof(T) == 2) {                      // (fp32 rows end at four)
-      if (vpt == 8) k = wide ? fp4_rows_kernel<T, NV, 8, true> : fp4_rows_kernel<T, NV, 8, false>;
+      if (vpt == 8) k = rows_kernel<T, NV, 8>(wide);
     }
     return launch(k, blocks, stream, x, M, K, ldx, q, ldq, sf, atoms, s_row, lg);
   }
