@@ -300,9 +300,9 @@ __device__ __forceinline__ void store_row_chunk_tma_t(const GemmArgs& g, const C
   }
   fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0 && n0 < g.N && m0 < g.M) {   // boxes wholly past the matrix are not issued
-    tma_store_2d(tm_c, base, n0, m0);
-    bulk_commit_group();
+  if (lane == 0) {
+    if (n0 < g.N && m0 < g.M) tma_store_2d(tm_c, base, n0, m0);   // boxes wholly past the matrix are not issued
+    bulk_commit_group();                     // (an empty group keeps the buffers' count in step)
   }
 }
 
@@ -359,9 +359,9 @@ __device__ __forceinline__ void store_row_chunk_staged_t(const GemmArgs& g, cons
   }
   fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0 && n0 < g.N && m0 < g.M) {   // boxes wholly past the matrix are not issued
-    tma_store_2d(tm_c, base, n0, m0);
-    bulk_commit_group();
+  if (lane == 0) {
+    if (n0 < g.N && m0 < g.M) tma_store_2d(tm_c, base, n0, m0);   // boxes wholly past the matrix are not issued
+    bulk_commit_group();                     // (an empty group keeps the buffers' count in step)
   }
 }
 
