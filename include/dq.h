@@ -488,8 +488,8 @@ DQ_API dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float
  *   dW [N, K] contiguous, bf16 (rounded once) or fp32; with `accumulate` (fp32
  *   only) both gradients are added to what dw and db hold.  db fp32 [N] or
  *   NULL.  Sums are fp32 on the bf16 tensor cores (tcgen05.mma kind::f16; both
- *   factors are exact bf16 numbers); their order is the schedule's and does
- *   not change from call to call.  M == 0 writes zeros (accumulate: nothing).
+ *   factors are exact bf16 numbers); their order is the schedule's (with db it
+ *   may be another than without) and does not change from call to call.  M == 0 writes zeros (accumulate: nothing).
  * Requirements: K % 16 == 0, N % 8 == 0, lddy % 8 == 0, M >= 0, M, N, K <=
  * 2^30; pointers 16-byte aligned (x: above).
  * ------------------------------------------------------------------------ */
