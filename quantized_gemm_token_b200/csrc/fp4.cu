@@ -653,9 +653,12 @@ dq_status make_tmap_sf(CUtensorMap* map, const uint8_t* sf, int64_t row_blocks, 
 
 // Two CTAs per SM.  All units resident at once share the memory's bandwidth
 // evenly and end together, whatever their number per SM, so only too few of
-// them call for a split.
+// them call for a split, and not one of less than eight stages (K = 1280, N =
+// 5120, one token: 4.1 us whole, 4.8 in two; K = 2048, N = 512: 4.1 in four, 4.7
+// in two).
 int few_splits(int nt, int kb_total, int sm_count) {
   int splits = 1;
+  if (kb_total < 8) return 1;
   while (splits < 8 && nt * splits <= sm_count && kb_total / (2 * splits) >= 2) splits *= 2;
   return splits;
 }
@@ -817,12 +820,12 @@ dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float* s_row
   const auto cs = reinterpret_cast<cudaStream_t>(stream);
   const bool nv = fmt == DQ_FP4_NV;
   const WaitCtl wait{d->err_word, wait_timeout_ns()};
-  // Few tokens: up to 32, or 64 without a split (K = 8192, N = 28672: 24.2,
-  // 25.7, 27.7 and 32.0 us at 1, 32, 64 and 128 tokens against the pair
-  // kernel's 44.6, 31.0, 31.9 and 33.1; K = N = 4096, split eight ways: 6.2,
-  // 7.5, 9.9 and 13.8 against 11.4, 9.4, 8.6 and 8.8).
-  const int nt = static_cast<int>((N + 127) / 128);
-  if (M <= 32 || (M <= 64 && few_splits(nt, static_cast<int>((K + F4_KE - 1) / F4_KE), d->sm_count) == 1)) {
+  // Few tokens: up to 32, or 64 where the pair kernel's tiles would leave SMs idle (long rows) or their ends would
+  // show (many channel tiles).  64 tokens, this kernel against the pair kernel: K = 8192, N = 512 6.6 us against
+  // 12.1, N = 4096 9.7 against 13.6, N = 28672 27.5 against 31.9; K = 4096, N = 4096 8.9 against 8.9; K = 1280, N =
+  // 28672 9.0 against 11.1, but N = 5120 6.9 against 6.1; 32 tokens: 5.4 against 5.9.
+  const int64_t nt = (N + 127) / 128;
+  if (M <= 32 || (M <= 64 && (K > 7 * F4_KE || nt >= d->sm_count))) {
     FewArgs f = {};
     f.M = static_cast<int>(M);
     f.N = static_cast<int>(N);
