@@ -459,16 +459,19 @@ auto rows_kernel(bool wide) {
 
 template <typename T, bool NV>
 dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* sf, float* s_row,
-                   cudaStream_t stream) {
+                   int sm_count, cudaStream_t stream) {
   const int64_t rows = (M + 127) / 128 * 128;
   const int64_t atoms = fp4_atoms(K, NV ? DQ_FP4_NV : DQ_FP4_MX);
   constexpr int V = 16 / sizeof(T);                      // elements per 16 bytes
   if (K <= 4096 * V && ldx % V == 0 && aligned(x, 16) && ldq % 8 == 0 && aligned(q, 8)) {
     // Runs per thread: four for NV and bf16 (fewer threads share the row maximum: 16384 x 8192 53.4 us against 57.5
-    // with two), two for MX (49.1 against 53.9 with four) and for fp32 (28672 x 8192 nv 151 against 179 with four), more
-    // where 256 threads would not hold the row; three, or for NV and bf16 five, where that leaves fewer idle places
-    // (65792 x 1280: nv 34.4 us with five, 44.3 with four; mx 33.0 with three, 37.9 with two).  Short rows share a warp
-    // (65792 x 64: 5.0 us, 14.8 with a warp per row).
+    // with two), two for MX (49.1 against 53.9 with four) and for fp32 (28672 x 8192 nv 151 against 179 with four),
+    // more where 256 threads would not hold the row; three, or for NV and bf16 five, where that leaves fewer idle
+    // places (65792 x 1280: nv 34.4 us with five, 44.3 with four; mx 33.0 with three, 37.9 with two) and still gives
+    // each SM two blocks (the layer of 1799 x 1280 -> 5120 nv, whose product starts beside the last blocks: 20.2 us
+    // with five, 17.5 with four).  Fewer runs where there would be fewer blocks than that (512 x 4096 nv 2.9 us, 3.2
+    // with four; with its product of 4096 channels 13.1, 14.2). Short rows share a warp (65792 x 64: 5.0 us, 14.8 with
+    // a warp per row).
     const int64_t nu = K / 16;
     constexpr bool four = NV && sizeof(T) == 2;
     auto threads_log2 = [nu](int v) {
@@ -479,9 +482,10 @@ dq_status quantize(const T* x, int64_t M, int64_t K, int64_t ldx, uint8_t* q, in
     int vpt = nu <= 32 ? 1 : four && nu > 64 ? 4 : 2;
     while ((static_cast<int64_t>(vpt) << 8) < nu) vpt *= 2;
     int lg = threads_log2(vpt);
+    while (vpt > 1 && vpt <= 4 && lg < 8 && rows >> (8 - lg) < 2 * sm_count) lg = threads_log2(vpt /= 2);
     for (int v = four ? 5 : 3; v >= 3 && nu > 32; v -= 2) {
       const int l = threads_log2(v);
-      if ((static_cast<int64_t>(v) << l) >= nu && 10 * (v << l) < 9 * (vpt << lg)) {
+      if ((static_cast<int64_t>(v) << l) >= nu && 10 * (v << l) < 9 * (vpt << lg) && rows >> (8 - l) >= 2 * sm_count) {
         vpt = v;
         lg = l;
       }
@@ -515,7 +519,8 @@ dq_status quantize_entry(const T* x, int64_t M, int64_t K, int64_t ldx, int fmt,
   if (st != DQ_OK) return st;
   if (M == 0) return DQ_OK;
   auto cs = reinterpret_cast<cudaStream_t>(stream);
-  return nv ? quantize<T, true>(x, M, K, ldx, q, ldq, sf, s, cs) : quantize<T, false>(x, M, K, ldx, q, ldq, sf, s, cs);
+  return nv ? quantize<T, true>(x, M, K, ldx, q, ldq, sf, s, d->sm_count, cs)
+            : quantize<T, false>(x, M, K, ldx, q, ldq, sf, s, d->sm_count, cs);
 }
 
 }  // namespace
