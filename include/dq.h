@@ -419,9 +419,10 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
  *     with an e4m3 scale d = e4m3(fp32((a / s) / 6)); code = e2m1(x / (d s))
  *     decided on the exact quotient, 0 where d = 0; the value is e2m1 * d * s.
  * Codes, block scales and row scales are bit-equal to a scalar evaluation of
- * these definitions, but for the sign of a zero code, which is free.  A block (MX) or row (NV) with a NaN or an infinity gets
- * a NaN scale (E = 255; s = NaN, its block scales and codes 0), so every
- * product computed from it is NaN.
+ * these definitions, but for the sign of a zero code, which is free.  A block
+ * (MX) or row (NV) with a NaN or an infinity gets a NaN scale (E = 255; s = NaN,
+ * its block scales and codes 0), so every product computed from it is NaN (NV:
+ * every product that is given the row scales).
  *
  * Block scales are stored in tiles of 128 rows x 4 blocks, 512 bytes each,
  * tile (row block, block group) row-major: byte 16 (r % 32) + 4 ((r % 128) /
@@ -444,8 +445,9 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
  *   cores (tcgen05.mma kind::mxf4nvf4.block_scale, fp32 accumulators);
  *   DQ_OUT_BF16: out = bf16(((acc * s_row[m]) * s_col[n]) + bias[n]), each op
  *   rounded on its own (s_row, s_col may be NULL: 1; bias NULL: no addition);
- *   DQ_OUT_F32: out = acc.  A, W contiguous.  The order of the fp32 sum is the
- *   hardware's and the schedule's; it does not change from call to call.
+ *   DQ_OUT_F32: out = acc, or NaN where s_row[m] or s_col[n] is NaN (the
+ *   scales have no other effect).  A, W contiguous.  The order of the fp32 sum
+ *   is the hardware's and the schedule's; it does not change from call to call.
  * Requirements: K % 32 == 0, N % 8 == 0, M >= 0, M, N, K <= 2^30; A, W, sf,
  * out, s_col and bias 16-byte aligned.
  * ------------------------------------------------------------------------ */

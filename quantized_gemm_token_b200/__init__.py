@@ -856,7 +856,7 @@ def dq_fp4_linear(A, sfa, s_row, W, sfw, s_col, bias=None, fmt="nv", out=None, o
     """out[M, N] = bf16(acc * s_row * s_col + bias) from 4-bit operands: A uint8
     [M, K/2] and W uint8 [N, K/2] with their tiled block scales, acc the
     block-scaled product on the tensor cores (or acc itself with
-    out_dtype="f32").  s_row / s_col may be None (1)."""
+    out_dtype="f32", NaN where a row scale is).  s_row / s_col may be None (1)."""
     code = _fp4_fmt(fmt)
     oc, odt = _f32_or_bf16(out_dtype)
     dev = _here(A, "A")

@@ -73,6 +73,24 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, ui
 #undef DQ_FP4_MMA
 }
 
+// fp32 output: the sum itself, but NaN where a row scale is: an NV row with a
+// NaN or an infinity has its NaN there alone (codes and block scales are 0).
+__device__ __forceinline__ float raw_sum(float acc, float s_row, float s_col) {
+  return isnan(s_row) || isnan(s_col) ? __uint_as_float(0x7fc00000u) : acc;
+}
+
+// The same for one row's 32 columns, whose scales lie at shared address `sc`.
+// One load and one vote per lane unless there is a NaN among the 32.
+__device__ __forceinline__ void raw_sums(uint32_t (&r)[32], float s_row, uint32_t sc, int lane) {
+  const uint32_t cols = __ballot_sync(0xffffffffu, isnan(__uint_as_float(pipe::lds32(sc + 4u * lane))));
+  const uint32_t bad = isnan(s_row) ? 0xffffffffu : cols;
+  if (__any_sync(0xffffffffu, bad != 0u)) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if ((bad >> j) & 1u) r[j] = 0x7fc00000u;
+  }
+}
+
 // ---------------------------------------------------------------- few tokens
 // The weight stream is the bound (0.53 - 0.56 bytes per weight at HBM rate),
 // so the weight's 128 channels sit on the MMA's M and the tokens on its N, one
@@ -291,13 +309,14 @@ __global__ void __launch_bounds__(FS_THREADS) fp4_few_kernel(const __grid_consta
       s = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
     }
     const int64_t o = static_cast<int64_t>(m) * g.N + ch;
-    if (g.raw) {
-      *reinterpret_cast<float4*>(static_cast<float*>(g.out) + o) = s;
-      continue;
-    }
     const float sr = g.s_row != nullptr ? __ldg(g.s_row + m) : 1.0f;
     float4 sc = make_float4(1.f, 1.f, 1.f, 1.f);
     if (g.s_col != nullptr) sc = __ldg(reinterpret_cast<const float4*>(g.s_col + ch));
+    if (g.raw) {
+      *reinterpret_cast<float4*>(static_cast<float*>(g.out) + o) =
+          make_float4(raw_sum(s.x, sr, sc.x), raw_sum(s.y, sr, sc.y), raw_sum(s.z, sr, sc.z), raw_sum(s.w, sr, sc.w));
+      continue;
+    }
     float y[4] = {__fmul_rn(__fmul_rn(s.x, sr), sc.x), __fmul_rn(__fmul_rn(s.y, sr), sc.y),
                   __fmul_rn(__fmul_rn(s.z, sr), sc.z), __fmul_rn(__fmul_rn(s.w, sr), sc.w)};
     if (g.bias != nullptr) {
@@ -594,7 +613,7 @@ __global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
         if (free_slot) {
           // the tile's column scales (unless there are none) and bias
           const int ncols = min(geo.width, g.N - n0);
-          const uint32_t sb = !g.out_s32 && g.s_col != nullptr ? static_cast<uint32_t>(ncols) * 4u : 0u;
+          const uint32_t sb = g.s_col != nullptr ? static_cast<uint32_t>(ncols) * 4u : 0u;
           const uint32_t bb = !g.out_s32 && g.bias != nullptr ? static_cast<uint32_t>(ncols) * 2u : 0u;
           mbar_arrive_expect_tx(smem_u32(sc_full), sb + bb);
           if (sb) bulk_load_1d(sc_slot, g.s_col + n0, sb, smem_u32(sc_full));
@@ -602,7 +621,7 @@ __global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
         }
       }
       if (!__all_sync(0xffffffffu, free_slot)) break;    // (a warp leaves whole)
-      const float srow = (!g.out_s32 && g.s_row != nullptr && m < g.M) ? __ldg(g.s_row + m) : 1.0f;
+      const float srow = (g.s_row != nullptr && m < g.M) ? __ldg(g.s_row + m) : 1.0f;
       if (!mbar_wait_warp(smem_u32(accf_bar), acc_phase, g.wait, abort_flag)) break;
       if (!mbar_wait_warp(smem_u32(sc_full), sc_phase, g.wait, abort_flag)) break;
       acc_phase ^= 1;
@@ -625,8 +644,10 @@ __global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
       for (int i = 0; i < C::CHUNKS; ++i) {
         const int c = grp + i * GROUPS;
         // a block wholly past the matrix is not stored and takes no buffer: the wait for a buffer counts stores
-        if (c < nch && n0 + c * 32 < g.N && m_slab < g.M)
+        if (c < nch && n0 + c * 32 < g.N && m_slab < g.M) {
+          if (g.out_s32) raw_sums(r[i], srow, sc_slot + static_cast<uint32_t>(c) * 128u, lane);
           store_row_chunk_staged<true>(g, &tm_c, next_buf(), lane, m_slab, n0 + c * 32, r[i], srow, sc_slot, c * 32);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(sc_free));
