@@ -380,7 +380,9 @@ struct CfgP {
   static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
 };
 
-template <bool NV>
+// RAW: fp32 output (a template switch: as a run-time test before each block's
+// store it cost bf16 output 0.4 - 0.8 us).
+template <bool NV, bool RAW>
 __global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ CUtensorMap tm_b2, const __grid_constant__ CUtensorMap tm_sa,
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(CfgP<NV>::THREADS, 1)
         const int c = grp + i * GROUPS;
         // a block wholly past the matrix is not stored and takes no buffer: the wait for a buffer counts stores
         if (c < nch && n0 + c * 32 < g.N && m_slab < g.M) {
-          if (g.out_s32) raw_sums(r[i], srow, sc_slot + static_cast<uint32_t>(c) * 128u, lane);
+          if constexpr (RAW) raw_sums(r[i], srow, sc_slot + static_cast<uint32_t>(c) * 128u, lane);
           store_row_chunk_staged<true>(g, &tm_c, next_buf(), lane, m_slab, n0 + c * 32, r[i], srow, sc_slot, c * 32);
         }
       }
@@ -796,7 +798,7 @@ dq_status launch_pair(const uint8_t* A, const uint8_t* sfa, const uint8_t* W, co
   if ((st = make_tmap_sf(&tsa, sfa, (g.M + 127) / 128, atoms, C::T, 1)) != DQ_OK) return st;
   if ((st = make_tmap_sf(&tsb, sfw, (g.N + 127) / 128, atoms, C::T, C::RB)) != DQ_OK) return st;
   if ((st = make_tmap_out_2d(&tc, g.out, g.N, g.M, g.out_s32 ? 4 : 2)) != DQ_OK) return st;
-  auto k = fp4_pair_kernel<NV>;
+  auto k = g.out_s32 ? fp4_pair_kernel<NV, true> : fp4_pair_kernel<NV, false>;
   if ((st = smem_limit_once(reinterpret_cast<const void*>(k), C::SMEM_BYTES)) != DQ_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, g.num_tiles)));
