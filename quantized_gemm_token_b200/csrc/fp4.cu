@@ -12,6 +12,15 @@
 // of tensor memory as the MMA wants them (column r / 32, lane r % 32,
 // replicated to the four sub-partitions); a tile serves one MMA (NV) or two
 // (MX, selected by the descriptor's scale id).
+//
+// Sums: the tensor core truncates when it adds an MMA's products (64 features)
+// to its fp32 accumulator: it loses less than 2^-23 of the sum so far, always
+// downwards.  A row is one chain, so |acc - exact| <= (ceil(K / 64) 2^-23 +
+// 2^-21) sum |a w| (2^-21: the additions of a split row).  Operands of one sign,
+// nv, pair kernel: 1.9e-6 of the sum at K = 8192, 8.8e-6 at 28672, 9.3e-5 at
+// 262144.  A chain taken to registers every 8192 features would lose 1.9e-6 at
+// any length and cost 1 us each time, the MMAs standing still (2048 x 16384 ->
+// 4096 58.3 -> 60.5 us): far below bf16 output's 2^-9, so it is not done.
 #include <cuda_bf16.h>
 
 #include <algorithm>
