@@ -494,7 +494,11 @@ DQ_API dq_status dq_fp4_linear(const uint8_t* A, const uint8_t* sfa, const float
  *   only) both gradients are added to what dw and db hold.  db fp32 [N] or
  *   NULL.  Sums are fp32 on the bf16 tensor cores (tcgen05.mma kind::f16; both
  *   factors are exact bf16 numbers); their order is the schedule's (with db it
- *   may be another than without) and does not change from call to call.  M == 0 writes zeros (accumulate: nothing).
+ *   may be another than without) and does not change from call to call.  The
+ *   tensor core truncates; chains end after 2048 tokens:
+ *     |dW - exact| <= (min(ceil(M / 16), 128) 2^-23 + (ceil(M / 2048) + 4) 2^-24) sum |dY x|,
+ *     |db - exact| <= (M / 16 + 48) 2^-24 sum |dY|.
+ *   M == 0 writes zeros (accumulate: nothing).
  * Requirements: K % 16 == 0, N % 8 == 0, lddy % 8 == 0, M >= 0, M, N, K <=
  * 2^30; pointers 16-byte aligned (x: above).
  * ------------------------------------------------------------------------ */

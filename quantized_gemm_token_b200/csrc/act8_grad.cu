@@ -26,11 +26,18 @@
 // Three rings, each as deep as its own round trip asks: dY in shared memory
 // (freed by the MMAs), codes in shared memory (freed by the converters), and
 // converted steps in tensor memory.
-// Sums: the tensor core truncates when it adds to its accumulator, so a chain
-// of MMAs loses about 2^-26 of the sum per instruction, all in one direction
-// (65792 tokens in one chain: 4.4e-5 of the result).  Every 2048 tokens the
+// Sums: the tensor core truncates when it adds an MMA's 16 tokens to its
+// accumulator, less than 2^-23 of the sum so far, all in one direction (65792
+// tokens in one chain: 4.4e-5 of the result).  Every 2048 tokens (128 MMAs) the
 // epilogue adds the accumulator to fp32 registers (rounding to nearest) and
-// the chain starts anew; the converted steps in flight cover the read.
+// the chain starts anew; the converted steps in flight cover the read.  So
+// |dW - exact| <= (min(ceil(M / 16), 128) 2^-23 + (ceil(M / 2048) + 4) 2^-24)
+// sum |dY x|.  The length is a choice between error and time.  Measured, chains
+// of 2048 against 1024 tokens: operands of one sign, 8192 tokens, 2.4e-6 against
+// 1.0e-6 of the sum (a library fp32 product 0.3e-6); zero-mean ones, relative
+// norm, 4.5e-7 against 2.1e-7 (1e-7 to 2e-7); 2048 x 4096 x 4096 57.4 against 61.5
+// us, 8192 x 4096 x 4096 198 against 209, 65792 x 1280 -> 5120 with db 655 against
+// 693.  dY itself carries bf16's 2^-9 per element.
 // db: in the tiles of the first 256 features the epilogue warps also add up
 // the dY tile that lies in shared memory (each lane eight channels), so dY is
 // not read again: there a stage's MMAs hand it to them, and they free it.
