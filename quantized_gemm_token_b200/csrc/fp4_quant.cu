@@ -10,9 +10,12 @@
 //       6 * 448), at least 2^-110; blocks of 16 features, ue4m3 scale d =
 //       e4m3(fp32(a / s / 6)), code = e2m1(x / (d s)) (0 where d = 0).
 // The row scale is a power of two so that x / s is exact and a code depends
-// on the exact quotient alone: a general fp32 scale would gain nothing (the
-// e4m3 block scale absorbs any factor below 2) and would round x / (d s)
-// twice.  A block (MX) or row (NV) that holds a NaN or an infinity gets the
+// on the exact quotient alone, where a general fp32 scale would round x / (d s)
+// twice.  It gives up little: the e4m3 block scale takes up a factor below 2,
+// but for the row's largest block, which a free scale max|row| / 2688 would give
+// the scale 448 exactly (relative error of a row, against a free scale: normal
+// values 9.50 % and 9.50 %, with 1 % of features twenty times larger 9.10 % and
+// 8.97 %, two features of 1024 a hundred times larger 6.0 % and 5.5 %).  A block (MX) or row (NV) that holds a NaN or an infinity gets the
 // scale NaN (E = 255; s = NaN with block scales and codes 0), so everything
 // computed from it is NaN.
 //

@@ -17,7 +17,7 @@ dq = pytest.importorskip("quantized_gemm_token_b200") if torch.cuda.is_available
 def test_every_step_of_the_block_scale(shift, neighbour):
     """Block maxima 6 d with d = 8 .. 15 sixteenths (times 64), so that each block's
     scale has the mantissa d / 8, and below each maximum all bf16 values from 2^-5
-    times it (far below the least border, 1 / 24 of it) up to it, at three places
+    times it (the least border is 1 / 24 of it) up to it, at three places
     of the exponent range; with a neighbour block the row scale is another one."""
     pats = (torch.arange(0x3a00, 0x4480, dtype=torch.int32) << 16).view(torch.float32)      # 2^-11 .. 2^10
     rows, steps = [], []
