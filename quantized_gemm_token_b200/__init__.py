@@ -924,14 +924,17 @@ def dq_act8_unpack(codes, scales, M: int, out=None, stream=None) -> torch.Tensor
     return out
 
 
-def dq_act8_weight_grad(dy, codes, scales, out=None, out_dtype="bf16", accumulate: bool = False, bias_grad=False,
+def dq_act8_weight_grad(dy, codes, scales, out=None, out_dtype=None, accumulate: bool = False, bias_grad=False,
                         stream=None):
     """(dW, db) of a linear layer from dy bf16 [M, N] (row stride dy.stride(0))
     and its input's 8-bit checkpoint: dW[n, k] = sum_m dy[m, n] x[m, k] as bf16
-    or fp32 [N, K], db[n] = sum_m dy[m, n] as fp32 [N].  `bias_grad`: False (db
+    or fp32 [N, K] (out_dtype; by default out's type, or bf16), db[n] = sum_m
+    dy[m, n] as fp32 [N].  `bias_grad`: False (db
     is None), True, or the fp32 tensor to fill.  With accumulate=True (fp32
     `out` given, and `bias_grad` a tensor or False) both are added to what the
     tensors hold."""
+    if out_dtype is None:
+        out_dtype = out.dtype if isinstance(out, torch.Tensor) else "bf16"
     oc, odt = _f32_or_bf16(out_dtype)
     dev = _here(dy, "dy")
     M, N, ld = _rows(dy, torch.bfloat16, "dy")
@@ -1066,7 +1069,7 @@ class Act8:
     def restore(self, out: torch.Tensor = None, stream=None) -> torch.Tensor:
         return dq_act8_unpack(self.codes, self.scales, self.M, out=out, stream=stream)
 
-    def weight_grad(self, dy: torch.Tensor, out: torch.Tensor = None, out_dtype="bf16", accumulate: bool = False,
+    def weight_grad(self, dy: torch.Tensor, out: torch.Tensor = None, out_dtype=None, accumulate: bool = False,
                     bias_grad=False, stream=None):
         if dy.shape[0] != self.M:
             raise ValueError(f"dy: {dy.shape[0]} tokens, the checkpoint holds {self.M}")
