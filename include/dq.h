@@ -433,7 +433,8 @@ DQ_API dq_status dq_s24_int8_linear(const int8_t* A, const float* s_row, int64_t
  * without a sign.
  *
  * dq_quantize_rows_fp4: x bf16 [M, K] (row stride ldx) -> q [M, K/2] (row
- *   stride ldq bytes), sf, s_row fp32 [M] (NV; ignored for MX, may be NULL).
+ *   stride ldq bytes; the product and the dequantizer below read ldq = K/2),
+ *   sf, s_row fp32 [M] (NV; ignored for MX, may be NULL).
  *   Rows with ldx % 8 == 0, a 16-byte aligned x, 8-byte aligned q and ldq and
  *   K <= 32768 take the single-pass kernel, others a slower one.
  * dq_quantize_weight_fp4: the same for fp32 rows (output channels); the
