@@ -15,9 +15,10 @@
 // but for the row's largest block, which a free scale max|row| / 2688 would give
 // the scale 448 exactly (relative error of a row, against a free scale: normal
 // values 9.50 % and 9.50 %, with 1 % of features twenty times larger 9.10 % and
-// 8.97 %, two features of 1024 a hundred times larger 6.0 % and 5.5 %).  A block (MX) or row (NV) that holds a NaN or an infinity gets the
-// scale NaN (E = 255; s = NaN with block scales and codes 0), so everything
-// computed from it is NaN.
+// 8.97 %, two features of 1024 a hundred times larger 6.0 % and 5.5 %).
+// A block (MX) or row (NV) that holds a NaN or an infinity gets the scale NaN
+// (E = 255; s = NaN with block scales and codes 0), so everything computed with
+// its scales is NaN.
 //
 // Both are bound by HBM: one pass over x, 0.53 or 0.56 bytes written for 2
 // read.  A row stays in registers between the row maximum and the codes.
